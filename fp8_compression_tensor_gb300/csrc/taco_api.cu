@@ -8,9 +8,9 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include "taco.h"
+#include "taco_host.h"
 #include "taco_kernels.h"
 
 namespace taco {
@@ -23,20 +23,7 @@ thread_local int t_last_cuda_error = 0;
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
-    std::once_flag once;
-    cudaError_t init_error = cudaSuccess;
-    int sm_count = 0;
-    uint32_t *fault = nullptr;  // device address of g_fault_flags
-    int ctas_per_sm = 0;        // last occupancy query (set-up check only)
-};
-
 DeviceState g_devices[kMaxDevices];
-
-bool block_supported(int block)
-{
-    return block == 32 || block == 64 || block == 128 || block == 256 || block == 512;
-}
 
 // Blocks 64 .. 512 run on the tensor-core kernels (512 as four rows of 128
 // elements per block), 32 on the lane-per-block codec; the shard reduce takes
@@ -51,12 +38,6 @@ bool tensor_core_block(int block)
 int view_row_elems(int block)
 {
     return block > 128 ? 128 : block;
-}
-
-taco_status_t cuda_fail(cudaError_t e)
-{
-    t_last_cuda_error = static_cast<int>(e);
-    return TACO_ERR_CUDA;
 }
 
 cudaError_t init_kernel(const KernelInfo &ki, int *ctas_per_sm)
@@ -102,7 +83,19 @@ void init_device(DeviceState &st)
     st.init_error = e;
 }
 
-// Set-up of the current device, once per device and process.
+}  // namespace
+
+bool block_supported(int block)
+{
+    return block == 32 || block == 64 || block == 128 || block == 256 || block == 512;
+}
+
+taco_status_t cuda_fail(cudaError_t e)
+{
+    t_last_cuda_error = static_cast<int>(e);
+    return TACO_ERR_CUDA;
+}
+
 taco_status_t device_state(DeviceState **out)
 {
     int dev = 0;
@@ -119,10 +112,13 @@ taco_status_t device_state(DeviceState **out)
     return TACO_OK;
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
+namespace {
+
 PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
 std::once_flag g_encode_once;
 cudaError_t g_encode_error = cudaSuccess;
+
+}  // namespace
 
 cudaError_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out)
 {
@@ -137,6 +133,8 @@ cudaError_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out)
     *out = g_encode_tiled;
     return g_encode_error;
 }
+
+namespace {
 
 // Tensor map of a bf16 tensor as [nblocks, block] rows, box {64 elements,
 // box_rows rows}, 128-byte swizzle; loads past the end read zeros, stores past
@@ -155,17 +153,6 @@ cudaError_t encode_block_rows_map(CUtensorMap *map, const void *x, int64_t nbloc
                               elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-bool aligned16(const void *p)
-{
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
-bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes)
-{
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
 }
 
 // Validates block and shape; on success sets the element count and packed bytes.

@@ -1,0 +1,150 @@
+// taco_train.cuh -- device-side building blocks of the training operators
+// (layer norm, GELU, weight gradient): typed loads and stores of eight
+// consecutive elements, checkpoint records and warp reductions.
+//
+// A checkpoint record is a DS-only record [codes | alpha = 1 | s] whose scale
+// is a power of two: s = 2^e with the least e >= -126 for which c = max|u| of
+// the block has c <= Q_max s.  The products q s of all three code formats then
+// hold at most eight significant bits, so they are exact in bf16 (above bf16's
+// subnormal range) and a tensor-core product with a checkpoint rounds nothing.
+// E4M3 and E5M2 keep their relative precision under any scale; INT8 gives up
+// at most one of its bits.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "taco_device.cuh"
+#include "taco_train.h"
+
+namespace taco {
+
+// ---------------------------------------------------------------------------
+// Typed elements
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Value i of a parameter array of run-time type (uniform over the grid).
+__device__ __forceinline__ float load_param(const void *p, int dtype, int64_t i)
+{
+    if (dtype == kTypeF32)
+        return static_cast<const float *>(p)[i];
+    if (dtype == kTypeF16)
+        return __half2float(static_cast<const __half *>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+
+__device__ __forceinline__ void store_param(void *p, int dtype, int64_t i, float v)
+{
+    if (dtype == kTypeF32)
+        static_cast<float *>(p)[i] = v;
+    else if (dtype == kTypeF16)
+        static_cast<__half *>(p)[i] = __float2half_rn(v);
+    else
+        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// Records
+// ---------------------------------------------------------------------------
+
+// Bits of max over non-negative floats given as |x|'s bit patterns: integer
+// order equals float order, and infinities and NaN sort above every finite
+// value, so a non-finite element is never lost in the maximum.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The block's scale from its maximum's bits: 2^e as above; 0 for an all-zero
+// block; NaN when an element is not finite, so that the block decodes to NaN.
+// *inv receives 1 / s (0 for a zero or non-finite block: all codes are zero).
+__device__ __forceinline__ float record_scale(uint32_t max_bits, int code, float *inv)
+{
+    // Q_max = mantissa * 2^shift with mantissa in [1, 2): 1.75 * 2^8, 1.75 * 2^15, 1.984375 * 2^6.
+    const int shift = code == 0 ? 8 : code == 1 ? 15 : 6;
+    const uint32_t mant = code == 2 ? 0x7e0000u : 0x600000u;
+    if (max_bits == 0u || max_bits >= 0x7f800000u) {
+        *inv = 0.f;
+        return max_bits == 0u ? 0.f : __uint_as_float(0x7fc00000u);
+    }
+    int e = static_cast<int>(max_bits >> 23) - 127 - shift + ((max_bits & 0x7fffffu) > mant ? 1 : 0);
+    e = max(e, -126);
+    *inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// Code byte of u / s (|u / s| <= Q_max; the product with the power of two 1/s is exact
+// or, for a subnormal u, exact as well).
+__device__ __forceinline__ uint8_t record_code(float u, float inv, int code)
+{
+    const float v = inv == 0.f ? 0.f : __fmul_rn(u, inv);
+    return static_cast<uint8_t>(encode4(code, v, 0.f, 0.f, 0.f) & 0xffu);
+}
+
+// The two values of the two code bytes in the low 16 bits of `pair`.
+__device__ __forceinline__ float2 codes2_to_float2(uint32_t pair, int code)
+{
+    if (code == 0)
+        return e4m3x2_to_float2(pair);
+    if (code == 1)
+        return e5m2x2_to_float2(pair);
+    return make_float2(static_cast<float>(static_cast<int8_t>(pair & 0xffu)),
+                       static_cast<float>(static_cast<int8_t>((pair >> 8) & 0xffu)));
+}
+
+// s / alpha of a record (alpha is 1 in the records written here).
+__device__ __forceinline__ float record_factor(const uint8_t *rec, int block)
+{
+    const uint2 m = *reinterpret_cast<const uint2 *>(rec + block);
+    const float alpha = __uint_as_float(m.x), s = __uint_as_float(m.y);
+    return alpha == 1.f ? s : __fdiv_rn(s, alpha);
+}
+
+// Value of element (row, col) of packed records of [rows, hidden].
+__device__ __forceinline__ float record_value(const uint8_t *packed, int64_t index, int block, int code)
+{
+    const int64_t k = index / block;
+    const uint8_t *rec = packed + k * (block + 8);
+    return codes2_to_float2(rec[index - k * block], code).x * record_factor(rec, block);
+}
+
+// ---------------------------------------------------------------------------
+// Reductions
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v += __shfl_xor_sync(kFullMask, v, d);
+    return v;
+}
+
+// Sum of v over the CTA (whole warps), the same for every thread; `part` holds
+// 32 floats and is free again after the call.
+__device__ __forceinline__ float cta_sum(float v, float *part)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    v = warp_sum(v);
+    if (lane == 0)
+        part[warp] = v;
+    __syncthreads();
+    v = warp_sum(lane < warps ? part[lane] : 0.f);
+    __syncthreads();
+    return v;
+}
+
+}  // namespace taco

@@ -80,7 +80,9 @@ typedef enum taco_status {
     TACO_ERR_OVERLAP = 6,           /* an output overlaps an input */
     TACO_ERR_CUDA = 7,              /* a CUDA runtime call or launch failed; see taco_last_cuda_error() */
     TACO_ERR_DEVICE_FAULT = 8,      /* taco_device_status(): a kernel gave up waiting */
-    TACO_ERR_BAD_OPTIONS = 9        /* the _ex calls: options NULL, or unknown variant or code format */
+    TACO_ERR_BAD_OPTIONS = 9        /* the _ex calls: options NULL, or unknown variant or code format;
+                                       the training calls: args NULL, unknown type, code or form, or
+                                       pointers given without the ones they belong to */
 } taco_status_t;
 
 #define TACO_MAX_SHARDS 16
@@ -176,10 +178,153 @@ TACO_API taco_status_t taco_reduce_shards_ex(const void *const *packed_shards, i
                                              int64_t hidden, const taco_options_t *options, void *packed_out,
                                              taco_stream_t stream);
 
+/* ------------------------------------------------------------------------- *
+ * Training operators around the compressed tensors: the layer norm behind a
+ * tensor-parallel AllReduce, GELU, and 8-bit checkpoints of the activations
+ * that a training step keeps from its forward to its backward pass.
+ *
+ * A checkpoint is a packed buffer of DS-only records (taco_variant_t) with
+ * alpha = 1 and a scale that is a power of two: for a block's values u with
+ * c = max|u|, s = 2^e with the least e >= -126 for which c <= Q_max s, and
+ * q = Cvt(u / s).  c = 0 gives s = 0 and all codes 0x00; a block with an
+ * infinity or a NaN gets s = NaN and decodes to NaN.  taco_decompress_ex with
+ * TACO_VARIANT_DS_ONLY decodes it; its values q s are exact in bf16 (above
+ * bf16's subnormal range).  The backward calls below take any DS-only records,
+ * also those of taco_compress_ex, and decode them as q (s / alpha).
+ *
+ * The common rules above hold, and:
+ *   - Tensors are row-major [rows, hidden] (leading dimensions flattened) of
+ *     `dtype`; `param_dtype` is the type of weights, biases and their gradients.
+ *   - Arithmetic, statistics and sums are binary32; outputs are rounded once
+ *     (nearest even).  Infinities and NaN propagate.
+ *   - hidden is a multiple of `block` where records are read or written; it is
+ *     free otherwise.
+ *   - Every result is the same from run to run (no floating-point atomics).
+ *   - Gradients of parameters sum over rows: with rows == 0 they are zeros
+ *     (the kernels that write them are launched).  hidden == 0 launches nothing.
+ *   - Workspaces hold nothing between calls; a call that gets fewer bytes than
+ *     its *_workspace() query returns TACO_ERR_BAD_SHAPE.
+ * ------------------------------------------------------------------------- */
+typedef enum taco_dtype {
+    TACO_DTYPE_BF16 = 0,
+    TACO_DTYPE_F16 = 1,
+    TACO_DTYPE_F32 = 2
+} taco_dtype_t;
+
+/*
+ * Layer norm of h = x, or of h = x + residual rounded to `dtype`:
+ *   mean = sum h / hidden, rstd = 1 / sqrt(sum (h - mean)^2 / hidden + eps),
+ *   xhat = (h - mean) rstd, y = xhat weight + bias.
+ */
+typedef struct taco_layernorm_args {
+    const void *x;              /* in:  [rows, hidden] */
+    const void *residual;       /* in:  [rows, hidden], or NULL */
+    const void *weight, *bias;  /* in:  [hidden] of param_dtype; NULL: 1 and 0 */
+    void *y;                    /* out: [rows, hidden] */
+    void *summed;               /* out: h, [rows, hidden]; non-NULL exactly when residual is */
+    float *mean, *rstd;         /* out: [rows] */
+    void *packed;               /* out: records of xhat, or NULL */
+    int64_t rows, hidden;
+    float eps;                  /* >= 0 */
+    int dtype, param_dtype;     /* taco_dtype_t */
+    int block, code;            /* of the records; read only when packed is non-NULL */
+} taco_layernorm_args_t;
+
+TACO_API taco_status_t taco_layernorm(const taco_layernorm_args_t *args, taco_stream_t stream);
+
+/*
+ * Gradients of the layer norm, with a = dy weight, c1 = sum a / hidden and
+ * c2 = sum a xhat / hidden: dx = rstd (a - c1 - xhat c2) + dsummed,
+ * dweight = sum over rows of dy xhat, dbias = sum over rows of dy.  xhat comes
+ * from x and mean (x = the tensor that was normalised: the forward call's
+ * `summed` where it had a residual), or from the records of the forward call.
+ */
+typedef struct taco_layernorm_backward_args {
+    const void *dy;             /* in:  [rows, hidden] */
+    const void *x;              /* in:  [rows, hidden], or NULL to read the records */
+    const float *mean;          /* in:  [rows]; NULL exactly when x is */
+    const float *rstd;          /* in:  [rows] */
+    const void *packed;         /* in:  records of xhat; non-NULL exactly when x is NULL */
+    const void *weight;         /* in:  [hidden], or NULL */
+    const void *dsummed;        /* in:  [rows, hidden] added to dx, or NULL */
+    void *dx;                   /* out: [rows, hidden] */
+    void *dweight, *dbias;      /* out: [hidden] of param_dtype; each may be NULL */
+    void *workspace;            /* needed when dweight or dbias is given */
+    int64_t workspace_bytes;
+    int64_t rows, hidden;
+    int dtype, param_dtype;
+    int block, code;            /* of the records */
+} taco_layernorm_backward_args_t;
+
+TACO_API int64_t taco_layernorm_backward_workspace(int64_t rows, int64_t hidden);   /* bytes; -1: bad shape */
+TACO_API taco_status_t taco_layernorm_backward(const taco_layernorm_backward_args_t *args, taco_stream_t stream);
+
+/*
+ * GELU of u = x + bias (binary32): y = u Phi(u), or with tanh_form
+ * y = u/2 (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))), and the records of u.
+ */
+typedef struct taco_gelu_args {
+    const void *x;              /* in:  [rows, hidden] */
+    const void *bias;           /* in:  [hidden] of param_dtype, or NULL */
+    void *y;                    /* out: [rows, hidden] */
+    void *packed;               /* out: records of u, or NULL */
+    int64_t rows, hidden;
+    int dtype, param_dtype;
+    int tanh_form;              /* 0 or 1 */
+    int block, code;            /* of the records; read only when packed is non-NULL */
+} taco_gelu_args_t;
+
+TACO_API taco_status_t taco_gelu(const taco_gelu_args_t *args, taco_stream_t stream);
+
+/* dx = dy gelu'(u) with u from the records, dbias = sum over rows of dx (before rounding), and y = gelu(u) again. */
+typedef struct taco_gelu_backward_args {
+    const void *dy;             /* in:  [rows, hidden] */
+    const void *packed;         /* in:  records of u */
+    void *dx;                   /* out: [rows, hidden] */
+    void *y;                    /* out: [rows, hidden], or NULL */
+    void *dbias;                /* out: [hidden] of param_dtype, or NULL */
+    void *workspace;            /* needed when dbias is given */
+    int64_t workspace_bytes;
+    int64_t rows, hidden;
+    int dtype, param_dtype;
+    int tanh_form;
+    int block, code;
+} taco_gelu_backward_args_t;
+
+TACO_API int64_t taco_gelu_backward_workspace(int64_t rows, int64_t hidden);   /* bytes; -1: bad shape */
+TACO_API taco_status_t taco_gelu_backward(const taco_gelu_backward_args_t *args, taco_stream_t stream);
+
+/*
+ * Weight gradient of a linear layer whose input X was kept as records:
+ *   dweight[m, n] = scale[n] sum_r dy[r, m] X[r, n] + dy_sum[m] shift[n]
+ *                   (+ dweight[m, n] as it was, when accumulate is 1).
+ * With scale and shift the weight and bias of a layer norm, the records of its
+ * xhat stand for its output; dy_sum[m] = sum_r dy[r, m] is the linear layer's
+ * bias gradient.  Records whose scale is not a power of two are decoded to bf16
+ * (nearest) for the product; those written here lose nothing.
+ */
+typedef struct taco_weight_grad_args {
+    const void *dy;             /* in:  bf16 [rows, out] */
+    const void *packed;         /* in:  records of X [rows, hidden] */
+    void *dweight;              /* out: [out, hidden] of dtype BF16 or F32 */
+    const void *scale, *shift;  /* in:  [hidden] of param_dtype; each may be NULL */
+    const float *dy_sum;        /* in:  [out]; non-NULL exactly when shift is */
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t rows, out, hidden;
+    int dtype, param_dtype;
+    int accumulate;             /* 0 or 1 */
+    int block, code;
+} taco_weight_grad_args_t;
+
+TACO_API int64_t taco_weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden);   /* bytes; -1: bad shape */
+TACO_API taco_status_t taco_weight_grad(const taco_weight_grad_args_t *args, taco_stream_t stream);
+
 /*
  * Synchronises `stream`, then reads and clears the current device's fault
  * flags (bit 0: compress, bit 1: decompress, bit 2: shard reduce gave up
- * waiting for a copy or a tile assignment; bit 3: the self-test below).
+ * waiting for a copy or a tile assignment; bit 3: the self-test below; bit 4:
+ * weight gradient).
  * *flags_out (may be NULL) receives them.  Returns TACO_ERR_DEVICE_FAULT if any
  * flag was set, TACO_ERR_CUDA if a CUDA call failed, TACO_OK otherwise.
  */
