@@ -12,6 +12,7 @@
 #include "taco.h"
 #include "taco_host.h"
 #include "taco_kernels.h"
+#include "taco_train.h"
 
 namespace taco {
 namespace {
@@ -80,6 +81,8 @@ void init_device(DeviceState &st)
             for (int k = 0; k < 6 && e == cudaSuccess; k++)
                 e = init_kernel(reduce_kernel_info(blocks[i], code, reduce_shards[k]), &st.ctas_per_sm);
     }
+    if (e == cudaSuccess)
+        e = init_weight_grad();
     st.init_error = e;
 }
 

@@ -64,6 +64,9 @@ struct WeightGradArgs {
     int dtype, param_dtype, accumulate, block, code, splits;
 };
 
+// Kernel attributes, once per device.
+cudaError_t init_weight_grad();
+
 cudaError_t launch_norm(int dtype, const NormArgs &a, int sms, cudaStream_t stream);
 // The gradient launches set nparts to the number of row chunks they use (at most what the caller gives).
 cudaError_t launch_norm_grad(int dtype, NormGradArgs *a, int sms, cudaStream_t stream);
