@@ -14,7 +14,7 @@
 // 256 tile of dW with tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 16 rows of
 // dY and X per instruction).  Both operands are MN-major: dY's rows hold M
 // contiguously and come by TMA (128-byte swizzle); X's rows hold N contiguously
-// and are decoded by four warps from record bytes to bf16 in the same layout,
+// and are decoded by eight warps from record bytes to bf16 in the same layout,
 // each CTA decoding the 128 columns that it feeds to the pair.  The pair halves
 // the decoding per product: a single CTA with M = 128 would decode each code for
 // half as many products.
@@ -26,9 +26,11 @@
 // warps then add it to the tile's sums, 128 registers a thread, while the next
 // chunk runs into the other half of tensor memory.
 //
-// Roles (512 threads): warp 0 loads dY, warp 1 of the even CTA issues the
-// products, warp 2 owns tensor memory, warps 4-7 decode, warps 8-15 add up and
-// write.
+// Roles (640 threads): warp 0 loads dY, warp 1 of the even CTA issues the
+// products, warp 2 owns tensor memory, warp 3 reports landed dY tiles to the
+// even CTA, warps 4-11 decode, warps 12-19 add up and write.  Two decoder warps
+// per scheduler hide each other's shared-memory, conversion and barrier
+// latencies.
 #include <algorithm>
 #include <climits>
 
@@ -144,9 +146,10 @@ constexpr int kChunkRows = 1024;              // rows per tensor-core accumulati
 constexpr int kStages = 5, kRawStages = 5;
 constexpr int kOperandBytes = 128 * kStageRows * 2;             // one CTA's A or B of a stage
 constexpr int kHalfBytes = 64 * kStageRows * 2;                 // 64 columns of it
-constexpr int kRawWarpBytes = 16 * 128 + 16 * 4 * 8;            // a decoder warp's 16 rows: codes, (alpha, s) pairs
-constexpr int kRawBytes = 4 * kRawWarpBytes;
-constexpr int kWgThreads = 512;
+constexpr int kDecoders = 8;                                     // decoder warps, 8 rows of a stage each
+constexpr int kRawWidth = 176;                                   // widest box of record bytes: 4 records of B = 32, and 8 bytes of slack
+constexpr int kRawBytes = kStageRows * (kRawWidth + 16);         // even rows, odd rows, then their scales where they lie apart
+constexpr int kWgThreads = 640;
 constexpr size_t kWgSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOperandBytes + kRawStages * kRawBytes + 512;
 constexpr uint32_t kIdesc = mma_idesc_bf16_f32(kPairM, kPairN) | (1u << 15) | (1u << 16);   // A and B MN-major
 
@@ -154,6 +157,8 @@ struct WgBarriers {
     uint64_t a_full[kStages];     // this CTA's dY tile has landed
     uint64_t full[kStages];       // even CTA: both CTAs' A and B of the stage are ready
     uint64_t empty[kStages];      // the stage's products are done
+    uint64_t raw_full[kRawStages];    // record bytes have landed
+    uint64_t raw_empty[kRawStages];   // and have been decoded
     uint64_t acc_full[2];         // a chunk's accumulator is complete
     uint64_t acc_empty[2];        // even CTA: both CTAs have read the accumulator
     uint32_t tmem;
@@ -181,31 +186,38 @@ __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr)
 
 __device__ __forceinline__ void cluster_arrive(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Bounded wait for a barrier that the other CTA's threads arrive on too.
+__device__ __forceinline__ bool cluster_try_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(TACO_WAIT_HINT_NS)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait for a barrier that the other CTA's threads arrive on too.  The
+// timer is read only after a first miss: the read alone costs more than a
+// stage's products.
 __device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, uint32_t *fault)
 {
+    if (cluster_try_wait(bar, parity))
+        return true;
     const uint64_t t0 = global_timer_ns();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(TACO_WAIT_HINT_NS)
-            : "memory");
-        if (ok)
-            return true;
+    while (!cluster_try_wait(bar, parity)) {
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             atomicOr(fault, kFaultWeightGrad);
             return false;
         }
     }
+    return true;
 }
-
 
 // MN-major operand in the 128-byte swizzled layout: rows of 64 MN-elements,
 // 8-row groups 1024 bytes apart, blocks of 64 MN-elements kHalfBytes apart.
@@ -238,18 +250,17 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
         : "memory");
 }
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
+// 16 consecutive tensor-memory columns of this thread's lane, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Copies 8 bytes, or zeros where `valid` is false (src is then not read).
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool valid)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 // Two codes (low 16 bits of `pair`) times f, rounded to bf16 (exact for a power of two).
@@ -292,9 +303,41 @@ struct WgPlan {
     }
 };
 
+// Where a CTA's 128 columns from n on lie in a record row, in bytes from the
+// start of the row in the map of its parity (see RawMaps).
+struct RawSpan {
+    int x[2], shift[2];               // box start (16-byte aligned) and first code's offset in the box: even rows, odd rows
+    int meta_x[2], meta_shift[2];     // the same for (alpha, s) of blocks above 128
+    __device__ RawSpan(int64_t n, int block, int odd_shift)
+    {
+        const int64_t at = n / block * (block + 8) + n % block, meta = n / block * (block + 8) + block;
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+            const int64_t c = at + p * odd_shift, m = meta + p * odd_shift;
+            x[p] = static_cast<int>(c & ~int64_t{15});
+            shift[p] = static_cast<int>(c & 15);
+            meta_x[p] = static_cast<int>(m & ~int64_t{15});
+            meta_shift[p] = static_cast<int>(m & 15);
+        }
+    }
+};
+
+// Record bytes come by TMA, 64 rows by a CTA's 128 columns at a time.  A record
+// row of an odd number of blocks has a length of 8 modulo 16, which no tensor
+// map takes as a stride; the rows of each parity lie two lengths apart, so each
+// parity has a map of its own.  The odd rows' map then starts 8 bytes before the
+// first of them (odd_shift = 8) to be 16-byte aligned.  No map reaches past the
+// buffer; rows and columns past the tensor read zeros.  Copying eight bytes a
+// lane with cp.async instead took 1.79 ms at 8192 x 16384 x 4096, this 0.84 ms.
+struct RawMaps {
+    CUtensorMap even, odd;            // boxes of `width` bytes by 32 rows
+    CUtensorMap meta_even, meta_odd;  // boxes of 16 bytes by 32 rows (blocks above 128)
+};
+
 template <int CODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
-taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, WeightGradArgs a, WgPlan plan, uint32_t *fault)
+taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ RawMaps raw_maps,
+                        WeightGradArgs a, WgPlan plan, int raw_width, int odd_shift, int odd_row0, uint32_t *fault)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) WgBarriers bars;
@@ -309,8 +352,12 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, WeightGradAr
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(bar(bars.a_full[s]), 1);
-            mbar_init(bar(bars.full[s]), 8);       // four decoder warps of each CTA
+            mbar_init(bar(bars.full[s]), 2 * (kDecoders + 1));   // each CTA's decoders, and its dY tile
             mbar_init(bar(bars.empty[s]), 1);
+        }
+        for (int s = 0; s < kRawStages; s++) {
+            mbar_init(bar(bars.raw_full[s]), 1);
+            mbar_init(bar(bars.raw_empty[s]), kDecoders);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(bar(bars.acc_full[b]), 1);
@@ -335,46 +382,50 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, WeightGradAr
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0 && lane == 0) {
             // dY: two boxes of 64 columns by 64 rows a stage
-            int64_t it = 0;
+            int s = 0;
+            uint32_t phase = 0, used = 0;
             bool ok = true;
             for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
                 int m0, n0, split, first, count;
                 plan.at(u, m0, n0, split, first, count);
                 const int x = m0 + static_cast<int>(rank) * 128;
-                for (int k = first; k < first + count; k++, it++) {
-                    const int s = static_cast<int>(it % kStages);
-                    if (it >= kStages && !mbar_wait_bounded_thread(bar(bars.empty[s]), static_cast<uint32_t>(it / kStages - 1) & 1u,
-                                                                   fault, kFaultWeightGrad)) {
+                for (int k = first; k < first + count; k++) {
+                    if (!mbar_wait_bounded_thread(bar(bars.empty[s]), phase ^ 1u, fault, kFaultWeightGrad)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = base + s * 2 * kOperandBytes;
-                    mbar_arrive_expect_tx(bar(bars.a_full[s]), kOperandBytes);
-                    tma_load_2d(dst, &map_dy, x, k * kStageRows, bar(bars.a_full[s]));
-                    tma_load_2d(dst + kHalfBytes, &map_dy, x + 64, k * kStageRows, bar(bars.a_full[s]));
+                    const uint32_t dst = base + s * 2 * kOperandBytes, full = bar(bars.a_full[s]);
+                    mbar_arrive_expect_tx(full, kOperandBytes);
+                    tma_load_2d(dst, &map_dy, x, k * kStageRows, full);
+                    tma_load_2d(dst + kHalfBytes, &map_dy, x + 64, k * kStageRows, full);
+                    used |= 1u << s;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
-            // no copy may land after the CTA is gone
-            for (int64_t i = it > kStages ? it - kStages : 0; i < it; i++)
-                mbar_wait_bounded_thread(bar(bars.a_full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u, fault,
-                                         kFaultWeightGrad);
+            // no copy may land after the CTA is gone: the last phase of every stage that was filled
+            for (int i = 0; i < kStages; i++)
+                if (used >> i & 1u)
+                    mbar_wait_bounded_thread(bar(bars.a_full[i]), i < s ? phase : phase ^ 1u, fault, kFaultWeightGrad);
         } else if (warp == 1 && lane == 0 && rank == 0) {
-            int64_t it = 0, chunk = 0;
+            int s = 0;
+            uint32_t phase = 0, chunk = 0;
             bool ok = true;
             for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
                 int m0, n0, split, first, count;
                 plan.at(u, m0, n0, split, first, count);
                 for (int k = 0; k < count && ok; chunk++) {
                     const int b = static_cast<int>(chunk & 1);
-                    if (chunk >= 2 && !cluster_wait(bar(bars.acc_empty[b]), static_cast<uint32_t>((chunk >> 1) - 1) & 1u, fault)) {
+                    if (chunk >= 2 && !cluster_wait(bar(bars.acc_empty[b]), ((chunk >> 1) - 1) & 1u, fault)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const int end = min(count, k + kChunkRows / kStageRows);
-                    for (const int begin = k; k < end; k++, it++) {
-                        const int s = static_cast<int>(it % kStages);
-                        if (!cluster_wait(bar(bars.full[s]), static_cast<uint32_t>(it / kStages) & 1u, fault)) {
+                    for (const int begin = k; k < end; k++) {
+                        if (!cluster_wait(bar(bars.full[s]), phase, fault)) {
                             ok = false;
                             break;
                         }
@@ -385,107 +436,153 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, WeightGradAr
                             pair_mma(tmem + b * kPairN, mn_desc(sa + j * 2048), mn_desc(sa + kOperandBytes + j * 2048),
                                      k > begin || j > 0);
                         pair_commit(bar(bars.empty[s]));
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
                     }
                     if (ok)
                         pair_commit(bar(bars.acc_full[b]));
                 }
             }
+        } else if (warp == 2 && lane == 0) {
+            // Record bytes
+            const uint32_t bytes = kStageRows * (raw_width + (a.block > 128 ? 16 : 0));
+            int s = 0;
+            uint32_t phase = 0, used = 0;
+            bool ok = true;
+            for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
+                int m0, n0, split, first, count;
+                plan.at(u, m0, n0, split, first, count);
+                const RawSpan at(n0 + static_cast<int64_t>(rank) * 128, a.block, odd_shift);
+                for (int k = first; k < first + count; k++) {
+                    if (!mbar_wait_bounded_thread(bar(bars.raw_empty[s]), phase ^ 1u, fault, kFaultWeightGrad)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = raw + s * kRawBytes, full = bar(bars.raw_full[s]);
+                    const int y = k * (kStageRows / 2);
+                    mbar_arrive_expect_tx(full, bytes);
+                    tma_load_2d(dst, &raw_maps.even, at.x[0], y, full);
+                    tma_load_2d(dst + kStageRows / 2 * kRawWidth, &raw_maps.odd, at.x[1], y + odd_row0, full);
+                    if (a.block > 128) {
+                        tma_load_2d(dst + kStageRows * kRawWidth, &raw_maps.meta_even, at.meta_x[0], y, full);
+                        tma_load_2d(dst + kStageRows * kRawWidth + 512, &raw_maps.meta_odd, at.meta_x[1], y + odd_row0, full);
+                    }
+                    used |= 1u << s;
+                    if (++s == kRawStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // no copy may land after the CTA is gone: the last phase of every slot that was filled
+            for (int i = 0; i < kRawStages; i++)
+                if (used >> i & 1u)
+                    mbar_wait_bounded_thread(bar(bars.raw_full[i]), i < s ? phase : phase ^ 1u, fault, kFaultWeightGrad);
+        } else if (warp == 3 && lane == 0) {
+            const uint32_t full0 = in_even_cta(bar(bars.full[0]));
+            int s = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
+                int m0, n0, split, first, count;
+                plan.at(u, m0, n0, split, first, count);
+                for (int k = 0; k < count; k++) {
+                    if (!mbar_wait_bounded_thread(bar(bars.a_full[s]), phase, fault, kFaultWeightGrad)) {
+                        ok = false;
+                        break;
+                    }
+                    cluster_arrive(full0 + s * 8);
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
         }
-    } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        // Decoders: warp d takes rows 16 d .. 16 d + 15 of every stage; lane l the
+    } else if (warp < 4 + kDecoders) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // Decoders: warp d takes rows 8 d .. 8 d + 7 of every stage; lane l the
         // codes 8 (l % 16) .. of rows l / 16, l / 16 + 2, ...
-        const int d = warp - 4, B = a.block, sub = lane >> 4, col = (lane & 15) * 8;
-        const int per_row = B < 128 ? 128 / B : 1;             // blocks of a row's 128 columns
-        const int64_t pitch = a.hidden / B * (B + 8);
-        const uint32_t my_raw = raw + d * kRawWarpBytes;
+        const int d = warp - 4, sub = lane >> 4, col = (lane & 15) * 8;
+        const int span = min(a.block, 128);                    // codes of a row's 128 columns lie in pieces of `span`
         const uint32_t swz = static_cast<uint32_t>(lane & 7);
         const uint32_t full0 = in_even_cta(bar(bars.full[0]));
-        // Producer position (the record bytes) and consumer position.
-        int64_t pu = first_unit, pit = 0;
-        int pk = 0, pcount = 0, pn = 0, pfirst = 0;
-        auto enter = [&]() {
-            if (pu < plan.units) {
-                int m0, split;
-                plan.at(pu, m0, pn, split, pfirst, pcount);
-                pn += static_cast<int>(rank) * 128;
-            }
-        };
-        auto produce = [&]() {
-            while (pu < plan.units && pk == pcount) {
-                pu += step_units;
-                pk = 0;
-                enter();
-            }
-            if (pu < plan.units) {
-                const uint32_t slot = my_raw + static_cast<uint32_t>(pit % kRawStages) * kRawBytes;
-                const int64_t r0 = static_cast<int64_t>(pfirst + pk) * kStageRows + d * 16;
-                const int64_t n = pn + col;
-                const uint8_t *src = a.packed + r0 * pitch + n / B * (B + 8) + n % B;
+        const uint32_t row_at = static_cast<uint32_t>(sub * (kStageRows / 2) * kRawWidth + d * 4 * raw_width);
+        const uint32_t meta_row_at = static_cast<uint32_t>(kStageRows * kRawWidth + sub * 512 + d * 64);
+        // Swizzled place of this lane's 16 bytes: row 8 d + 2 j + sub.
+        uint32_t place[4];
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const int row = 2 * j + sub;
-                    const bool valid = n < a.hidden && r0 + row < a.rows;
-                    copy8(slot + row * 128 + col, valid ? src + row * pitch : a.packed, valid);
-                }
-                for (int i = lane; i < 16 * per_row; i += 32) {
-                    const int row = i / per_row;
-                    const int64_t nb = pn + static_cast<int64_t>(i % per_row) * B;
-                    const bool valid = nb < a.hidden && r0 + row < a.rows;
-                    copy8(slot + 2048 + i * 8, valid ? a.packed + (r0 + row) * pitch + nb / B * (B + 8) + B : a.packed, valid);
-                }
-                pk++;
-                pit++;
-            }
-            cp_async_commit();
-        };
-        enter();
-        for (int i = 0; i < kRawStages - 1; i++)
-            produce();
-        int64_t it = 0;
+        for (int j = 0; j < 4; j++) {
+            const uint32_t kr = static_cast<uint32_t>(2 * j + sub);
+            place[j] = static_cast<uint32_t>(kOperandBytes + (col >> 6) * kHalfBytes + d * 1024) + kr * 128 + ((swz ^ kr) << 4);
+        }
+        int s = 0, slot = 0;
+        uint32_t phase = 0, raw_phase = 0;
         bool ok = true;
         for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
             int m0, n0, split, first, count;
             plan.at(u, m0, n0, split, first, count);
-            for (int k = 0; k < count; k++, it++) {
-                const int s = static_cast<int>(it % kStages);
-                __syncwarp();                                  // every lane has read the slot that produce() refills
-                produce();
-                cp_async_wait<kRawStages - 1>();
-                __syncwarp();
-                if (it >= kStages && !mbar_wait_bounded(bar(bars.empty[s]), static_cast<uint32_t>(it / kStages - 1) & 1u, fault,
-                                                        kFaultWeightGrad)) {
+            const RawSpan at(n0 + static_cast<int64_t>(rank) * 128, a.block, odd_shift);
+            const uint32_t code_at = row_at + at.shift[sub] + col / span * (span + 8) + col % span;
+            const uint32_t meta_at = a.block > 128 ? meta_row_at + at.meta_shift[sub]
+                                                   : row_at + at.shift[sub] + col / span * (span + 8) + span;
+            const uint32_t meta_pitch = a.block > 128 ? 16u : static_cast<uint32_t>(raw_width);
+            for (int k = 0; k < count; k++) {
+                if (!mbar_wait_bounded(bar(bars.raw_full[slot]), raw_phase, fault, kFaultWeightGrad)) {
                     ok = false;
                     break;
                 }
-                const uint32_t slot = my_raw + static_cast<uint32_t>(it % kRawStages) * kRawBytes;
-                const uint32_t dst = base + s * 2 * kOperandBytes + kOperandBytes + (col >> 6) * kHalfBytes;
+                const uint32_t src = raw + static_cast<uint32_t>(slot) * kRawBytes;
+                uint2 c[4], meta[4];
+                uint32_t other = 0;                            // nonzero where some alpha is not 1
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const int row = 2 * j + sub, kr = d * 16 + row;
-                    const uint2 c = lds64(slot + row * 128 + col);
-                    const uint2 meta = lds64(slot + 2048 + (row * per_row + (per_row > 1 ? col / B : 0)) * 8);
-                    const float alpha = __uint_as_float(meta.x);
-                    float f = __uint_as_float(meta.y);
-                    if (alpha != 1.f && f != 0.f)
-                        f = __fdiv_rn(f, alpha);
-                    sts128(dst + (kr >> 3) * 1024 + (kr & 7) * 128 + ((swz ^ (kr & 7)) << 4), decode8<CODE>(c, f));
+                for (int j = 0; j < 4; j++) {
+                    c[j] = lds64(src + code_at + j * raw_width);
+                    meta[j] = lds64(src + meta_at + j * meta_pitch);
                 }
-                fence_proxy_async_smem();
-                if (!mbar_wait_bounded(bar(bars.a_full[s]), static_cast<uint32_t>(it / kStages) & 1u, fault, kFaultWeightGrad)) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    other |= meta[j].y ? meta[j].x ^ 0x3f800000u : 0u;   // s = 0: all zero, as past the tensor's end
+                if (__any_sync(kFullMask, other != 0u)) {      // records of compress
+#pragma unroll 1
+                    for (int i = 0; i < 4; i++) {
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            if (i == j && meta[j].y)
+                                meta[j].y = __float_as_uint(__fdiv_rn(__uint_as_float(meta[j].y), __uint_as_float(meta[j].x)));
+                    }
+                }
+                __syncwarp();                                  // the warp has read the slot
+                if (lane == 0)
+                    mbar_arrive(bar(bars.raw_empty[slot]));
+                if (!mbar_wait_bounded(bar(bars.empty[s]), phase ^ 1u, fault, kFaultWeightGrad)) {
                     ok = false;
                     break;
                 }
+                const uint32_t dst = base + s * 2 * kOperandBytes;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    sts128(dst + place[j], decode8<CODE>(c[j], __uint_as_float(meta[j].y)));
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     cluster_arrive(full0 + s * 8);
+                if (++slot == kRawStages) {
+                    slot = 0;
+                    raw_phase ^= 1u;
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
         }
-        cp_async_wait<0>();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        // Epilogue: warp w reads lanes 32 (w % 4) .., columns 128 (w / 4 - 2) .. of the accumulators.
-        const int quarter = warp & 3, half = (warp - 8) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        // Epilogue: warp w reads lanes 32 (w % 4) .., columns 128 (w / 4 - 3) .. of the accumulators.
+        const int quarter = warp & 3, half = (warp - 12) >> 2;
         const uint32_t empty0 = in_even_cta(bar(bars.acc_empty[0]));
         int64_t chunk = 0;
         bool ok = true;
@@ -505,14 +602,12 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, WeightGradAr
                 tc_fence_after_sync();
                 const uint32_t src = tmem + (static_cast<uint32_t>(quarter) << 21) + b * kPairN + half * 128;
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t r[32];
-                    tmem_ld32(src + c * 32, r);
-                    tmem_ld_wait();
-                    tmem_regs_ready(r);
+                for (int c = 0; c < 8; c++) {
+                    uint32_t r[16];
+                    tmem_ld16(src + c * 16, r);
 #pragma unroll
-                    for (int i = 0; i < 32; i++)
-                        acc[c * 32 + i] += __uint_as_float(r[i]);
+                    for (int i = 0; i < 16; i++)
+                        acc[c * 16 + i] += __uint_as_float(r[i]);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
@@ -586,6 +681,23 @@ cudaError_t launch_pairs(const void *fn, int pairs, cudaStream_t stream, void **
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// Tensor map of [rows, width] elements `pitch` bytes apart, boxes {box_x, box_y}; what lies outside reads zeros.
+cudaError_t encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t width, int64_t rows, int64_t pitch,
+                      int box_x, int box_y, CUtensorMapSwizzle swizzle)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const cudaError_t e = tensor_map_encoder(&encode);
+    if (e != cudaSuccess)
+        return e;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y)}, elem_strides[2] = {1, 1};
+    return encode(map, type, 2, const_cast<void *>(base), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 // The tensor-core kernel's TMA view of dY needs rows of a multiple of 16 bytes.
 bool on_tensor_cores(int64_t out) { return out % 8 == 0; }
 
@@ -614,7 +726,7 @@ int weight_grad_splits(int64_t rows, int64_t out, int64_t hidden)
 bool weight_grad_in_range(int64_t rows, int64_t out, int64_t hidden)
 {
     // 32-bit TMA coordinates, whole tiles and stages past the end included
-    return rows <= INT32_MAX - 64 && out <= INT32_MAX - 256 && hidden <= INT32_MAX - 256 && (out + kTile - 1) / kTile <= INT32_MAX / ((hidden + kTile - 1) / kTile + 1);
+    return rows <= INT32_MAX - 64 && out <= INT32_MAX - 256 && hidden <= INT32_MAX / 2 && (out + kTile - 1) / kTile <= INT32_MAX / ((hidden + kTile - 1) / kTile + 1);
 }
 
 cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream)
@@ -625,25 +737,34 @@ cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms
         const int64_t tiles = (a.hidden + kTile - 1) / kTile * ((a.out + kTile - 1) / kTile);
         return launch_kernel(reinterpret_cast<void *>(&taco_weight_grad_any_kernel), static_cast<int>(tiles), 256, 0, stream, p);
     }
-    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    cudaError_t e = tensor_map_encoder(&encode);
+    alignas(64) CUtensorMap map;
+    alignas(64) RawMaps raw;
+    const int64_t pitch = a.hidden / a.block * (a.block + 8);
+    int odd_shift = static_cast<int>(pitch & 8);
+    // A row's 128 columns: 128 codes, with (alpha, s) inside up to B = 128, and 8 bytes of slack.
+    int raw_width = a.block > 128 ? 144 : (128 / a.block * (a.block + 8) + 8 + 15) / 16 * 16;
+    const int64_t even_rows = (a.rows + 1) / 2, odd_rows = a.rows / 2;
+    int odd_row0 = odd_rows ? 0 : 1;   // a single row: the odd map holds it too, read from row 1 on, which is outside
+    const uint8_t *odd_base = odd_rows ? a.packed + pitch - odd_shift : a.packed;
+    cudaError_t e = encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.dy, a.out, a.rows, 2 * a.out, 64, kStageRows,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int i = 0; i < 2 && e == cudaSuccess; i++) {
+        const int width = i ? 16 : raw_width;
+        e = encode_2d(i ? &raw.meta_even : &raw.even, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.packed, pitch, even_rows, 2 * pitch, width,
+                      kStageRows / 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (e == cudaSuccess)
+            e = encode_2d(i ? &raw.meta_odd : &raw.odd, CU_TENSOR_MAP_DATA_TYPE_UINT8, odd_base, odd_rows ? pitch + odd_shift : pitch,
+                          std::max<int64_t>(odd_rows, 1), 2 * pitch, width, kStageRows / 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
     if (e != cudaSuccess)
         return e;
-    alignas(64) CUtensorMap map;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.out), static_cast<cuuint64_t>(a.rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.out) * 2};
-    const cuuint32_t box[2] = {64, kStageRows}, elem_strides[2] = {1, 1};
-    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(a.dy), dims, strides, box, elem_strides,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
     WgPlan plan;
     plan.tiles_m = static_cast<int>((a.out + kPairM - 1) / kPairM);
     plan.tiles_n = static_cast<int>((a.hidden + kPairN - 1) / kPairN);
     plan.stages_total = static_cast<int>((a.rows + kStageRows - 1) / kStageRows);
     plan.splits = a.splits;
     plan.units = static_cast<int64_t>(plan.tiles_m) * plan.tiles_n * a.splits;
-    void *p[] = {&map, &args, &plan, &fault};
+    void *p[] = {&map, &raw, &args, &plan, &raw_width, &odd_shift, &odd_row0, &fault};
     e = launch_pairs(wg_kernel(a.code), static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
     if (e == cudaSuccess && a.splits > 1) {
         void *q[] = {&args};
