@@ -83,6 +83,8 @@ void init_device(DeviceState &st)
     }
     if (e == cudaSuccess)
         e = init_weight_grad();
+    if (e == cudaSuccess)
+        e = init_norm();
     st.init_error = e;
 }
 

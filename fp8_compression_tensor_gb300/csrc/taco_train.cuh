@@ -39,6 +39,102 @@ __device__ __forceinline__ __half from_float<__half>(float v) { return __float2h
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Eight consecutive elements as loaded (16 bytes, or 32 for binary32).
+template <typename T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T *p)
+{
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); i++)
+        r.v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<float> &r, float (&f)[8])
+{
+    const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        f[i] = __uint_as_float(w[i]);
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16> &r, float (&f)[8])
+{
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<__half> &r, float (&f)[8])
+{
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 v = f16x2_to_float2(w[i]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+}
+
+__device__ __forceinline__ Raw8<float> pack8(const float (&f)[8], const float *)
+{
+    Raw8<float> r;
+    r.v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    r.v[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+    return r;
+}
+
+__device__ __forceinline__ Raw8<__nv_bfloat16> pack8(const float (&f)[8], const __nv_bfloat16 *)
+{
+    Raw8<__nv_bfloat16> r;
+    r.v[0] = make_uint4(float2_to_bf16x2(f[0], f[1]), float2_to_bf16x2(f[2], f[3]), float2_to_bf16x2(f[4], f[5]),
+                        float2_to_bf16x2(f[6], f[7]));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t float2_to_f16x2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ Raw8<__half> pack8(const float (&f)[8], const __half *)
+{
+    Raw8<__half> r;
+    r.v[0] = make_uint4(float2_to_f16x2(f[0], f[1]), float2_to_f16x2(f[2], f[3]), float2_to_f16x2(f[4], f[5]),
+                        float2_to_f16x2(f[6], f[7]));
+    return r;
+}
+
+// Rounds to T and stores eight consecutive elements.
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&f)[8])
+{
+    const Raw8<T> r = pack8(f, static_cast<const T *>(nullptr));
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); i++)
+        reinterpret_cast<uint4 *>(p)[i] = r.v[i];
+}
+
+// Eight consecutive parameters of run-time type from i on (i a multiple of 8).
+__device__ __forceinline__ void load_param8(const void *p, int dtype, int64_t i, float (&f)[8])
+{
+    if (dtype == kTypeF32)
+        unpack8(load_raw8(static_cast<const float *>(p) + i), f);
+    else if (dtype == kTypeF16)
+        unpack8(load_raw8(static_cast<const __half *>(p) + i), f);
+    else
+        unpack8(load_raw8(static_cast<const __nv_bfloat16 *>(p) + i), f);
+}
+
 // Value i of a parameter array of run-time type (uniform over the grid).
 __device__ __forceinline__ float load_param(const void *p, int dtype, int64_t i)
 {
@@ -103,6 +199,91 @@ __device__ __forceinline__ float2 codes2_to_float2(uint32_t pair, int code)
         return e5m2x2_to_float2(pair);
     return make_float2(static_cast<float>(static_cast<int8_t>(pair & 0xffu)),
                        static_cast<float>(static_cast<int8_t>((pair >> 8) & 0xffu)));
+}
+
+// Eight code bytes as floats.
+__device__ __forceinline__ void codes8_to_float(uint2 c, int code, float (&f)[8])
+{
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        float2 a, b;
+        if (code == 2) {
+            int8x4_to_float(w[h], a, b);
+        } else if (code == 0) {
+            a = e4m3x2_to_float2(w[h] & 0xffffu);
+            b = e4m3x2_to_float2(w[h] >> 16);
+        } else {
+            a = e5m2x2_to_float2(w[h] & 0xffffu);
+            b = e5m2x2_to_float2(w[h] >> 16);
+        }
+        f[4 * h] = a.x, f[4 * h + 1] = a.y, f[4 * h + 2] = b.x, f[4 * h + 3] = b.y;
+    }
+}
+
+// Factor s / alpha of a record's (alpha, s).
+__device__ __forceinline__ float meta_factor(uint2 m)
+{
+    const float alpha = __uint_as_float(m.x), s = __uint_as_float(m.y);
+    return alpha == 1.f ? s : __fdiv_rn(s, alpha);
+}
+
+__device__ __forceinline__ uint32_t max_abs_bits8(const float (&f)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        m = max(m, abs_bits(f[i]));
+    return m;
+}
+
+// Writes the records of NV vectors of eight values a lane.  Vector j of a warp
+// holds 256 consecutive elements, lane l those from 8 l on, so a block of B <=
+// 256 lies in B / 8 neighbouring lanes of one vector and a block of 512 in a
+// pair of vectors (an even j and j + 1).  at[j] is the first code's address; a
+// lane whose at[j] is null takes no part (whole blocks only).
+template <int NV>
+__device__ __forceinline__ void write_records(const float (&u)[NV][8], uint8_t *const (&at)[NV], int block, int code)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t top[NV];
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        top[j] = max_abs_bits8(u[j]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+            if (8 * d < block)
+                top[j] = max(top[j], __shfl_xor_sync(kFullMask, top[j], d));
+    }
+    if (NV > 1 && block == 512) {
+#pragma unroll
+        for (int j = 0; j + 1 < NV; j += 2)
+            top[j] = top[j + 1] = max(top[j], top[j + 1]);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+        float inv;
+        const float s = record_scale(top[j], code, &inv);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            v[i] = inv == 0.f ? 0.f : __fmul_rn(u[j][i], inv);
+        const uint2 q = make_uint2(encode4(code, v[0], v[1], v[2], v[3]), encode4(code, v[4], v[5], v[6], v[7]));
+        if (at[j]) {
+            *reinterpret_cast<uint2 *>(at[j]) = q;
+            // the lane that holds the block's last codes writes (alpha, s) behind them
+            const int from = lane * 8 + (block == 512 ? (j & 1) * 256 : 0);
+            if ((from & (block - 1)) + 8 == block)
+                *reinterpret_cast<float2 *>(at[j] + 8) = make_float2(1.f, s);
+        }
+    }
+}
+
+// Byte of element `col` in a record row.
+__device__ __forceinline__ int64_t record_offset(int64_t col, int block)
+{
+    const int64_t k = col / block;
+    return k * (block + 8) + (col - k * block);
 }
 
 // s / alpha of a record (alpha is 1 in the records written here).
