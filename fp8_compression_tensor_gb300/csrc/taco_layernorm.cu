@@ -95,22 +95,6 @@ __device__ __forceinline__ void group_barrier(int id, int threads)
     asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sum over the `warps` warps of a row group, the same for all its threads.
-// `part` is the group's own; the caller alternates between two of them, so one
-// barrier a sum is enough: a thread writes a part again only behind the next
-// sum's barrier, when every thread has read it.
-__device__ __forceinline__ float group_sum(float v, float *part, int warp, int warps, int barrier_id)
-{
-    v = warp_sum(v);
-    if (warps == 1)
-        return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0)
-        part[warp] = v;
-    group_barrier(barrier_id, warps * 32);
-    return warp_sum(lane < warps ? part[lane] : 0.f);
-}
-
 // 1 / sqrt(v): the hardware's estimate and one Newton step.
 __device__ __forceinline__ float inv_sqrt(float v)
 {
@@ -118,99 +102,191 @@ __device__ __forceinline__ float inv_sqrt(float v)
     return v > 0.f && v < 3.0e38f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
-constexpr int kNormThreads = 1024;
-constexpr int kGradThreads = 512;
+constexpr int kRowThreadsMax = 512;
 
-// A group of `warps` warps holds a row in registers: NV vectors of eight
-// elements a lane, vector j of warp w from column 256 (w NV + j) on.  The CTA's
-// groups take rows in turn; weight and bias are read from global memory once,
-// into shared memory (STAGED; with one row a group, straight from global
-// memory), and the next row's loads are in flight while this row is reduced.
-template <typename T, int NV, bool STAGED>
-__global__ void __launch_bounds__(kNormThreads, 1) taco_norm_kernel(NormArgs a, int warps, int groups)
+// Rows come to shared memory `stages` rows ahead by cp.async, 16 bytes at a
+// time.  Each thread copies exactly the pieces of x, dy and the like that it
+// will read itself, so these need no barrier, only the thread's own wait.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
 {
-    extern __shared__ float sparam[];              // weight, then bias, `hidden` each (STAGED)
-    __shared__ float parts[2][32];
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// The same, reading `bytes` of the 16 and writing zeros for the others.
+__device__ __forceinline__ void copy16_part(uint32_t to, const void *from, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the newest `ahead` rows' copies of this thread have landed.
+__device__ __forceinline__ void copies_landed(int ahead)
+{
+    if (ahead == 3)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (ahead == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (ahead == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Eight binary32 values in shared memory.
+__device__ __forceinline__ F8 load_shared8(const float *p)
+{
+    return unpack(Raw8<float>{{*reinterpret_cast<const uint4 *>(p), *reinterpret_cast<const uint4 *>(p + 4)}});
+}
+
+// A row's columns over a group of `warps` warps: vector j (of NV) of warp w
+// starts at column 256 (w NV + j), lane l holds eight columns from 8 l on.  The
+// CTA's groups work on rows of their own.  Many columns a thread keep the two
+// row sums cheap: 32 a thread run 8192 x 4096 bf16 in REPLACE_FWD, eight a thread
+// (twice the warps, two rows a pass) in 51 us.
+//
+// Statistics with one barrier: each warp sums its values and then their squared
+// distances from its own mean p_w = S_w / n_w; with the row's mean m the sum of
+// squares is sum_w M_w + n_w (p_w - m)^2.  `sums` alternates between two sets, so
+// a set is written again only behind the next row's barrier.
+//
+// weight and bias stay in shared memory (STAGED) where a CTA has several rows
+// to read them for.
+template <typename T, int NV, bool STAGED>
+__global__ void __launch_bounds__(kRowThreadsMax, 1) taco_norm_kernel(NormArgs a, int warps, int groups, int stages)
+{
+    extern __shared__ __align__(16) uint8_t dynamic[];   // weight, bias (STAGED), then the copies
+    __shared__ float2 sums[2][16];
     grid_launch_dependents();
+    constexpr int kUnits = sizeof(T) / 2;                 // 16-byte units of eight elements
     const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
-    const int C = static_cast<int>(a.hidden);
-    float *part0 = parts[0] + group * warps, *part1 = parts[1] + group * warps;
-    const float inv_c = 1.f / static_cast<float>(C);
+    const int C = static_cast<int>(a.hidden), unit = blockDim.x * 16;
+    const float fc = static_cast<float>(C);
+    float *sparam = reinterpret_cast<float *>(dynamic);
+    const uint8_t *ring = dynamic + (STAGED ? 8 * C : 0) + threadIdx.x * 16;
+    const uint32_t ring_at = smem_addr(ring);
+    const int row_units = (a.residual ? 2 : 1) * NV * kUnits;
+    const int warp_n = min(max(C - warp * 256 * NV, 0), 256 * NV), lane_n = min(max(C - (lane & 15) * 256 * NV, 0), 256 * NV);
+    const float warp_inv = warp_n > 0 ? 1.f / static_cast<float>(warp_n) : 0.f;
+    const float lane_inv = lane_n > 0 ? 1.f / static_cast<float>(lane_n) : 0.f;   // of warp lane % 16
+    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     int col[NV];
 #pragma unroll
     for (int j = 0; j < NV; j++)
         col[j] = ((warp * NV + j) * 32 + lane) * 8;
     grid_dependency_wait();
-    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
-    int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-    Raw8<T> nx[NV], nr[NV];
-    auto fetch = [&](int64_t r) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group, step = static_cast<int64_t>(gridDim.x) * groups;
+    auto copy_row = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            uint32_t to = ring_at + static_cast<uint32_t>(stage * row_units * unit);
+            auto piece = [&](const T *src) {
 #pragma unroll
-        for (int j = 0; j < NV; j++)
-            if (r < a.rows && col[j] < C) {
-                nx[j] = load_raw8(x + r * C + col[j]);
-                if (res)
-                    nr[j] = load_raw8(res + r * C + col[j]);
-            }
+                for (int j = 0; j < NV; j++)
+#pragma unroll
+                    for (int k = 0; k < kUnits; k++, to += unit)
+                        if (col[j] < C)
+                            copy16(to, reinterpret_cast<const uint4 *>(src + row * C + col[j]) + k);
+            };
+            piece(x);
+            if (res)
+                piece(res);
+        }
+        copies_issued();
     };
-    fetch(row);
+    for (int i = 0; i < stages - 1; i++)
+        copy_row(first + i * step, i);
     if (STAGED) {
         for (int c = threadIdx.x * 8; c < C; c += blockDim.x * 8) {
             float f[8];
             if (a.weight) {
                 load_param8(a.weight, a.param_dtype, c, f);
-                for (int i = 0; i < 8; i++)
-                    sparam[c + i] = f[i];
+                store8(sparam + c, f);
             }
             if (a.bias) {
                 load_param8(a.bias, a.param_dtype, c, f);
-                for (int i = 0; i < 8; i++)
-                    sparam[C + c + i] = f[i];
+                store8(sparam + C + c, f);
             }
         }
         __syncthreads();
     }
-    for (; row < a.rows; row += step) {
-        float h[NV][8];
-        float sum = 0.f;
+    auto param = [&](const void *p, int offset, int c) {
+        if (STAGED)
+            return load_shared8(sparam + offset + c);
+        float f[8];
+        load_param8(p, a.param_dtype, c, f);
+        return F8{{make_float2(f[0], f[1]), make_float2(f[2], f[3]), make_float2(f[4], f[5]), make_float2(f[6], f[7])}};
+    };
+    int stage = 0, fill = stages - 1;
+    uint32_t side = 0;
+    for (int64_t row = first; row < a.rows; row += step, side ^= 1u) {
+        copy_row(row + (stages - 1) * step, fill);
+        fill = fill + 1 == stages ? 0 : fill + 1;
+        copies_landed(stages - 1);
+        const uint8_t *mine = ring + static_cast<size_t>(stage) * row_units * unit;
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        F8 h[NV];
+        float2 total = both(0.f);
 #pragma unroll
-        for (int j = 0; j < NV; j++) {
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                h[j][i] = 0.f;
+        for (int j = 0; j < NV; j++)
             if (col[j] < C) {
-                unpack8(nx[j], h[j]);
+                Raw8<T> v;
+#pragma unroll
+                for (int k = 0; k < kUnits; k++)
+                    v.v[k] = *reinterpret_cast<const uint4 *>(mine + (j * kUnits + k) * unit);
+                h[j] = unpack(v);
                 if (res) {
-                    float r[8];
-                    unpack8(nr[j], r);
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        h[j][i] += r[i];
-                    const Raw8<T> o = pack8(h[j], x);
+                    for (int k = 0; k < kUnits; k++)
+                        v.v[k] = *reinterpret_cast<const uint4 *>(mine + ((NV + j) * kUnits + k) * unit);
+                    const F8 r = unpack(v);
 #pragma unroll
-                    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); i++)
-                        reinterpret_cast<uint4 *>(static_cast<T *>(a.summed) + row * C + col[j])[i] = o.v[i];
-                    unpack8(o, h[j]);
+                    for (int i = 0; i < 4; i++)
+                        h[j].v[i] = add2(h[j].v[i], r.v[i]);
+                    v = pack<T>(h[j]);
+                    store_raw8(static_cast<T *>(a.summed) + row * C + col[j], v);
+                    h[j] = unpack(v);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    sum += h[j][i];
+                for (int i = 0; i < 4; i++)
+                    total = add2(total, h[j].v[i]);
             }
-        }
-        fetch(row + step);
-        const float mean = group_sum(sum, part0, warp, warps, 1 + group) / static_cast<float>(C);   // exact for constant rows
-        float sq = 0.f;
+        float sum = warp_sum(total.x + total.y);
+        const float pivot = sum * warp_inv;
+        float2 squares = both(0.f);
 #pragma unroll
         for (int j = 0; j < NV; j++)
             if (col[j] < C) {
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    h[j][i] -= mean;
-                    sq = fmaf(h[j][i], h[j][i], sq);
+                for (int i = 0; i < 4; i++) {
+                    const float2 d = add2(h[j].v[i], both(-pivot));
+                    squares = fma2(d, d, squares);
                 }
             }
-        const float rstd = inv_sqrt(fmaf(group_sum(sq, part1, warp, warps, 1 + group), inv_c, a.eps));
+        float sq = warp_sum(squares.x + squares.y), mean;
+        if (warps > 1) {
+            float2 *mine_sums = sums[side] + group * warps;
+            if (lane == 0)
+                mine_sums[warp] = make_float2(sum, sq);
+            group_barrier(1 + group, warps * 32);
+            // at most 16 warps: the two halves of the warp add the same 16 values
+            const int w = lane & 15;
+            const float2 v = w < warps ? mine_sums[w] : make_float2(0.f, 0.f);
+            sum = v.x;
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1)
+                sum += __shfl_xor_sync(kFullMask, sum, d);
+            mean = sum / fc;
+            const float d = v.x * lane_inv - mean;
+            sq = fmaf(static_cast<float>(lane_n) * d, d, v.y);
+#pragma unroll
+            for (int d2 = 8; d2 > 0; d2 >>= 1)
+                sq += __shfl_xor_sync(kFullMask, sq, d2);
+        } else {
+            mean = sum / fc;
+            const float d = pivot - mean;
+            sq = fmaf(fc * d, d, sq);
+        }
+        const float rstd = inv_sqrt(sq / fc + a.eps);
         if (warp == 0 && lane == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
@@ -218,42 +294,26 @@ __global__ void __launch_bounds__(kNormThreads, 1) taco_norm_kernel(NormArgs a, 
 #pragma unroll
         for (int j = 0; j < NV; j++)
             if (col[j] < C) {
-                float y[8];
+                F8 y;
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    y[i] = h[j][i] *= rstd;
+                for (int i = 0; i < 4; i++)
+                    y.v[i] = h[j].v[i] = mul2(add2(h[j].v[i], both(-mean)), both(rstd));
                 if (a.weight) {
-                    float w[8];
-                    if (STAGED)
-                        unpack8(Raw8<float>{{*reinterpret_cast<const uint4 *>(sparam + col[j]),
-                                             *reinterpret_cast<const uint4 *>(sparam + col[j] + 4)}}, w);
-                    else
-                        load_param8(a.weight, a.param_dtype, col[j], w);
+                    const F8 w = param(a.weight, 0, col[j]);
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        y[i] *= w[i];
+                    for (int i = 0; i < 4; i++)
+                        y.v[i] = mul2(y.v[i], w.v[i]);
                 }
                 if (a.bias) {
-                    float b[8];
-                    if (STAGED)
-                        unpack8(Raw8<float>{{*reinterpret_cast<const uint4 *>(sparam + C + col[j]),
-                                             *reinterpret_cast<const uint4 *>(sparam + C + col[j] + 4)}}, b);
-                    else
-                        load_param8(a.bias, a.param_dtype, col[j], b);
+                    const F8 b = param(a.bias, C, col[j]);
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        y[i] += b[i];
+                    for (int i = 0; i < 4; i++)
+                        y.v[i] = add2(y.v[i], b.v[i]);
                 }
-                store8(static_cast<T *>(a.y) + row * C + col[j], y);
+                store_raw8(static_cast<T *>(a.y) + row * C + col[j], pack<T>(y));
             }
-        if (a.packed) {
-            uint8_t *at[NV];
-            const int64_t pitch = record_offset(C, a.block);
-#pragma unroll
-            for (int j = 0; j < NV; j++)
-                at[j] = col[j] < C ? a.packed + row * pitch + record_offset(col[j], a.block) : nullptr;
-            write_records<NV>(h, at, a.block, a.code);
-        }
+        if (a.packed)
+            write_records<NV>(h, col, C, a.packed + row * (C / a.block) * (a.block + 8), a.block, a.code);
     }
 }
 
@@ -292,207 +352,206 @@ __global__ void __launch_bounds__(kRowThreads) taco_norm_grad_any_kernel(NormGra
     }
 }
 
-// Rows of whole vectors, the same layout of a row over a group of warps as the
-// forward pass, so a thread keeps its columns and adds up their dweight and
-// dbias in registers over all rows that its group takes.  Each thread copies its
-// own pieces of the next rows (dy, x, dsummed) to shared memory with cp.async,
-// `stages` rows deep, and reads only what it copied itself, so the copies need
-// no barrier; a row's two sums need one.  Codes and scales of records, 8 bytes
-// each, are loaded to registers a row ahead.
+// The forward pass's layout, so a thread keeps its columns and adds up their
+// dweight and dbias in registers over all rows that its group takes.  The
+// pieces of a row are read from shared memory twice, for the row's two sums and
+// for dx, rather than held in registers next to these sums.
+//
+// Record bytes (RECORDS) are copied by the whole group, 16 at a time from the
+// 16-byte boundary below the row's first one, so they are read behind a barrier:
+// the one of the row sums of the row before, ahead of which each thread waits
+// for its part of the next row.  A row's place is filled again behind the
+// barrier of the row after it, when every thread has left it.
 template <typename T, int NV, bool RECORDS>
-__global__ void __launch_bounds__(kGradThreads, 1)
+__global__ void __launch_bounds__(kRowThreadsMax, 1)
 taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
 {
-    extern __shared__ __align__(16) uint8_t dynamic[];
-    __shared__ float2 parts[2][32];
+    extern __shared__ __align__(16) uint8_t dynamic[];   // weight, then the copies
+    __shared__ float2 sums[2][16];
     grid_launch_dependents();
+    constexpr int kUnits = sizeof(T) / 2;
     const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
-    const int C = static_cast<int>(a.hidden), nthreads = blockDim.x;
-    constexpr int kUnits = sizeof(T) / 2;            // 16-byte units of eight elements
-    const int per_stage = (1 + !RECORDS + (a.dsummed != nullptr)) * NV * kUnits;
+    const int C = static_cast<int>(a.hidden), unit = blockDim.x * 16;
+    const int row_units = (1 + !RECORDS + (a.dsummed != nullptr)) * NV * kUnits;
+    const int shift = RECORDS ? 31 - __clz(a.block) : 0;
+    const int64_t pitch = RECORDS ? static_cast<int64_t>(C >> shift) * (a.block + 8) : 0;
+    const int record_room = RECORDS ? static_cast<int>(pitch + 8 + 15) / 16 * 16 : 0;     // of one group's row
+    const int stage_bytes = row_units * unit + groups * record_room;
+    const float inv_c = 1.f / static_cast<float>(C);
     float *sweight = reinterpret_cast<float *>(dynamic);
-    uint4 *ring = reinterpret_cast<uint4 *>(dynamic + (a.weight ? (C * 4 + 15) / 16 * 16 : 0));
-    const uint32_t ring_at = smem_addr(ring) + threadIdx.x * 16;
+    uint8_t *ring = dynamic + (a.weight ? 4 * C : 0);
+    const uint32_t ring_at = smem_addr(ring);
     int col[NV];
-    int64_t rec[NV], meta[NV];
 #pragma unroll
-    for (int j = 0; j < NV; j++) {
+    for (int j = 0; j < NV; j++)
         col[j] = ((warp * NV + j) * 32 + lane) * 8;
-        if (RECORDS) {
-            rec[j] = record_offset(col[j], a.block);
-            meta[j] = static_cast<int64_t>(col[j] / a.block) * (a.block + 8) + a.block;
-        }
-    }
-    const int64_t pitch = RECORDS ? record_offset(C, a.block) : 0;
     grid_dependency_wait();
-    if (a.weight) {
-        for (int c = threadIdx.x * 8; c < C; c += nthreads * 8) {
-            float f[8];
-            load_param8(a.weight, a.param_dtype, c, f);
-            for (int i = 0; i < 8; i++)
-                sweight[c + i] = f[i];
-        }
-        __syncthreads();
-    }
     const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group, step = static_cast<int64_t>(gridDim.x) * groups;
     auto copy_row = [&](int64_t row, int stage) {
         if (row < a.rows) {
-            uint32_t to = ring_at + static_cast<uint32_t>(stage * per_stage * nthreads) * 16u;
+            uint32_t to = ring_at + static_cast<uint32_t>(stage * stage_bytes) + threadIdx.x * 16u;
             auto piece = [&](const void *src) {
 #pragma unroll
                 for (int j = 0; j < NV; j++)
 #pragma unroll
-                    for (int k = 0; k < kUnits; k++, to += nthreads * 16)
+                    for (int k = 0; k < kUnits; k++, to += unit)
                         if (col[j] < C)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
-                                         "l"(reinterpret_cast<const uint4 *>(static_cast<const T *>(src) + row * C + col[j]) + k)
-                                         : "memory");
+                            copy16(to, reinterpret_cast<const uint4 *>(static_cast<const T *>(src) + row * C + col[j]) + k);
             };
             piece(a.dy);
             if (!RECORDS)
                 piece(a.x);
             if (a.dsummed)
                 piece(a.dsummed);
+            if (RECORDS) {
+                const int64_t at = row * pitch & ~int64_t{15}, left = a.rows * pitch - at;
+                const int bytes = static_cast<int>((row + 1) * pitch - at);
+                const uint32_t room = ring_at + static_cast<uint32_t>(stage * stage_bytes + row_units * unit + group * record_room);
+                for (int c = (warp * 32 + lane) * 16; c < bytes; c += warps * 512)
+                    copy16_part(room + c, a.packed + at + c, left - c < 16 ? 8 : 16);
+            }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        copies_issued();
     };
-    uint2 codes[NV], scales[NV];
     float next_rstd = 0.f, next_mean = 0.f;
     auto fetch = [&](int64_t row) {
-        if (row >= a.rows)
-            return;
-        next_rstd = __ldg(a.rstd + row);
-        if (!RECORDS)
-            next_mean = __ldg(a.mean + row);
-        if (RECORDS) {
-#pragma unroll
-            for (int j = 0; j < NV; j++)
-                if (col[j] < C) {
-                    codes[j] = __ldg(reinterpret_cast<const uint2 *>(a.packed + row * pitch + rec[j]));
-                    scales[j] = __ldg(reinterpret_cast<const uint2 *>(a.packed + row * pitch + meta[j]));
-                }
+        if (row < a.rows) {
+            next_rstd = __ldg(a.rstd + row);
+            if (!RECORDS)
+                next_mean = __ldg(a.mean + row);
         }
     };
-    float dw[NV][8], db[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; j++)
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            dw[j][i] = db[j][i] = 0.f;
     for (int i = 0; i < stages - 1; i++)
         copy_row(first + i * step, i);
     fetch(first);
+    if (a.weight) {
+        for (int c = threadIdx.x * 8; c < C; c += blockDim.x * 8) {
+            float f[8];
+            load_param8(a.weight, a.param_dtype, c, f);
+            store8(sweight + c, f);
+        }
+    }
+    if (RECORDS)
+        copies_landed(stages - 2);
+    __syncthreads();
+    F8 dw[NV], db[NV];
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            dw[j].v[i] = db[j].v[i] = both(0.f);
     int stage = 0, fill = stages - 1;
     uint32_t side = 0;
     for (int64_t row = first; row < a.rows; row += step, side ^= 1u) {
-        copy_row(row + (stages - 1) * step, fill);
-        fill = fill + 1 == stages ? 0 : fill + 1;
-        if (stages == 4)
-            asm volatile("cp.async.wait_group 3;" ::: "memory");
-        else if (stages == 3)
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-        else if (stages == 2)
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        const uint4 *mine = ring + threadIdx.x + static_cast<size_t>(stage) * per_stage * nthreads;
+        if (!RECORDS) {
+            copy_row(row + (stages - 1) * step, fill);
+            copies_landed(stages - 1);
+        }
+        const uint8_t *mine = ring + static_cast<size_t>(stage) * stage_bytes + threadIdx.x * 16;
+        const uint8_t *rec = ring + static_cast<size_t>(stage) * stage_bytes + row_units * unit + group * record_room +
+                             (RECORDS ? row * pitch & 15 : 0);
         stage = stage + 1 == stages ? 0 : stage + 1;
         const float rstd = next_rstd, mean = next_mean;
-        uint2 q[NV];
-        float factor[NV];
-        if (RECORDS) {
-#pragma unroll
-            for (int j = 0; j < NV; j++) {
-                q[j] = codes[j];
-                factor[j] = meta_factor(scales[j]);
-            }
-        }
         fetch(row + step);
-        // Vector j of the thread's piece `tensor`, and xhat of vector j.
-        auto vector = [&](int tensor, int j, float (&f)[8]) {
-            Raw8<T> r;
+        // Vector j of the row's piece `tensor`; xhat and dy weight of vector j.
+        auto vector = [&](int tensor, int j) {
+            Raw8<T> v;
 #pragma unroll
             for (int k = 0; k < kUnits; k++)
-                r.v[k] = mine[static_cast<size_t>((tensor * NV + j) * kUnits + k) * nthreads];
-            unpack8(r, f);
+                v.v[k] = *reinterpret_cast<const uint4 *>(mine + ((tensor * NV + j) * kUnits + k) * unit);
+            return unpack(v);
         };
-        auto normalised = [&](int j, float (&f)[8]) {
+        auto normalised = [&](int j) {
+            F8 f;
             if (RECORDS) {
-                codes8_to_float(q[j], a.code, f);
+                const uint8_t *block = rec + (col[j] >> shift) * (a.block + 8);
+                f = codes8_to_float(*reinterpret_cast<const uint2 *>(block + (col[j] & (a.block - 1))), a.code);
+                const float s = meta_factor(*reinterpret_cast<const uint2 *>(block + a.block));
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    f[i] *= factor[j];
+                for (int i = 0; i < 4; i++)
+                    f.v[i] = mul2(f.v[i], both(s));
             } else {
-                vector(1, j, f);
+                f = vector(1, j);
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    f[i] = (f[i] - mean) * rstd;
+                for (int i = 0; i < 4; i++)
+                    f.v[i] = mul2(add2(f.v[i], both(-mean)), both(rstd));
             }
+            return f;
         };
-        auto weighted = [&](int j, const float (&g)[8], float (&f)[8]) {
-            if (a.weight) {
-                const float4 lo = *reinterpret_cast<const float4 *>(sweight + col[j]), hi = *reinterpret_cast<const float4 *>(sweight + col[j] + 4);
-                f[0] = g[0] * lo.x, f[1] = g[1] * lo.y, f[2] = g[2] * lo.z, f[3] = g[3] * lo.w;
-                f[4] = g[4] * hi.x, f[5] = g[5] * hi.y, f[6] = g[6] * hi.z, f[7] = g[7] * hi.w;
-            } else {
+        auto weighted = [&](int j, const F8 &g) {
+            if (!a.weight)
+                return g;
+            F8 f = load_shared8(sweight + col[j]);
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    f[i] = g[i];
-            }
+            for (int i = 0; i < 4; i++)
+                f.v[i] = mul2(f.v[i], g.v[i]);
+            return f;
         };
-        float s1 = 0.f, s2 = 0.f;
+        float2 t1 = both(0.f), t2 = both(0.f);
 #pragma unroll
         for (int j = 0; j < NV; j++)
             if (col[j] < C) {
-                float g[8], xh[8], w[8];
-                vector(0, j, g);
-                normalised(j, xh);
-                weighted(j, g, w);
+                const F8 w = weighted(j, vector(0, j)), xh = normalised(j);
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    s1 += w[i];
-                    s2 = fmaf(w[i], xh[i], s2);
+                for (int i = 0; i < 4; i++) {
+                    t1 = add2(t1, w.v[i]);
+                    t2 = fma2(w.v[i], xh.v[i], t2);
                 }
             }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (warps > 1) {
-            float2 *part = parts[side] + group * warps;
-            if (lane == 0)
-                part[warp] = make_float2(s1, s2);
-            group_barrier(1 + group, warps * 32);
-            const float2 v = lane < warps ? part[lane] : make_float2(0.f, 0.f);
-            s1 = warp_sum(v.x);
-            s2 = warp_sum(v.y);
+        float s1 = t1.x + t1.y, s2 = t2.x + t2.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            s1 += __shfl_xor_sync(kFullMask, s1, d);
+            s2 += __shfl_xor_sync(kFullMask, s2, d);
         }
-        const float c1 = s1 / static_cast<float>(C), c2 = s2 / static_cast<float>(C);
+        if (RECORDS)
+            copies_landed(stages - 3);
+        if (warps > 1) {
+            float2 *mine_sums = sums[side] + group * warps;
+            if (lane == 0)
+                mine_sums[warp] = make_float2(s1, s2);
+            group_barrier(1 + group, warps * 32);
+            const int w = lane & 15;
+            const float2 v = w < warps ? mine_sums[w] : make_float2(0.f, 0.f);
+            s1 = v.x;
+            s2 = v.y;
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) {
+                s1 += __shfl_xor_sync(kFullMask, s1, d);
+                s2 += __shfl_xor_sync(kFullMask, s2, d);
+            }
+        } else if (RECORDS) {
+            __syncwarp();
+        }
+        if (RECORDS)
+            copy_row(row + (stages - 1) * step, fill);
+        fill = fill + 1 == stages ? 0 : fill + 1;
+        const float c1 = s1 * inv_c, c2 = s2 * inv_c;
 #pragma unroll
         for (int j = 0; j < NV; j++)
             if (col[j] < C) {
-                float g[8], xh[8], w[8];
-                vector(0, j, g);
-                normalised(j, xh);
-                weighted(j, g, w);
+                const F8 g = vector(0, j), xh = normalised(j);
+                F8 w = weighted(j, g);
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    dw[j][i] = fmaf(g[i], xh[i], dw[j][i]);
-                    db[j][i] += g[i];
-                    w[i] = rstd * fmaf(-xh[i], c2, w[i] - c1);
+                for (int i = 0; i < 4; i++) {
+                    dw[j].v[i] = fma2(g.v[i], xh.v[i], dw[j].v[i]);
+                    db[j].v[i] = add2(db[j].v[i], g.v[i]);
+                    w.v[i] = mul2(fma2(xh.v[i], both(-c2), add2(w.v[i], both(-c1))), both(rstd));
                 }
                 if (a.dsummed) {
-                    vector(RECORDS ? 1 : 2, j, g);
+                    const F8 s = vector(RECORDS ? 1 : 2, j);
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        w[i] += g[i];
+                    for (int i = 0; i < 4; i++)
+                        w.v[i] = add2(w.v[i], s.v[i]);
                 }
-                store8(static_cast<T *>(a.dx) + row * C + col[j], w);
+                store_raw8(static_cast<T *>(a.dx) + row * C + col[j], pack<T>(w));
             }
     }
     if (!a.parts)
         return;
-    // The groups' sums, added in order in the ring's place.
-    float *sums = reinterpret_cast<float *>(ring);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // The groups' sums, added in order in the copies' place: for each column eighth four pairs of dweight, four of dbias.
+    float2 *acc = reinterpret_cast<float2 *>(ring);
+    copies_landed(0);
     for (int g = 0; g < groups; g++) {
         __syncthreads();
         if (g == group) {
@@ -500,19 +559,20 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
             for (int j = 0; j < NV; j++)
                 if (col[j] < C) {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
+                    for (int i = 0; i < 4; i++) {
+                        float2 *w = acc + i * (C / 8) + col[j] / 8, *b = w + C / 2;
                         if (g > 0) {
-                            dw[j][i] += sums[(i * 2) * (C / 8) + col[j] / 8];
-                            db[j][i] += sums[(i * 2 + 1) * (C / 8) + col[j] / 8];
+                            dw[j].v[i] = add2(dw[j].v[i], *w);
+                            db[j].v[i] = add2(db[j].v[i], *b);
                         }
                         if (g + 1 < groups) {
-                            sums[(i * 2) * (C / 8) + col[j] / 8] = dw[j][i];
-                            sums[(i * 2 + 1) * (C / 8) + col[j] / 8] = db[j][i];
+                            *w = dw[j].v[i];
+                            *b = db[j].v[i];
                         }
                     }
                     if (g + 1 == groups) {
-                        store8(a.parts + static_cast<int64_t>(blockIdx.x) * C + col[j], dw[j]);
-                        store8(a.parts + static_cast<int64_t>(a.nparts + blockIdx.x) * C + col[j], db[j]);
+                        store_raw8(a.parts + static_cast<int64_t>(blockIdx.x) * C + col[j], pack<float>(dw[j]));
+                        store_raw8(a.parts + static_cast<int64_t>(a.nparts + blockIdx.x) * C + col[j], pack<float>(db[j]));
                     }
                 }
         }
@@ -575,34 +635,58 @@ int row_grid(int64_t rows, int sms, int per_sm)
     return static_cast<int>(rows < cap ? rows : cap);
 }
 
-// Whole vectors of eight, and at most 32 warps of two vectors a lane.
-constexpr int kMaxVectorWidth = 32 * 2 * 256;
+// Whole vectors of eight, and at most 16 warps of four vectors a lane.
+constexpr int kMaxVectorWidth = 16 * 4 * 256;
+constexpr size_t kMaxShared = 225 * 1024;
 
 bool fits_registers(int64_t hidden) { return hidden % 8 == 0 && hidden <= kMaxVectorWidth; }
+
+// Vectors a lane: four, or what a single warp needs for a short row.
+int lane_vectors(int64_t hidden) { return hidden <= 256 ? 1 : hidden <= 512 ? 2 : 4; }
+
+// Row groups of a CTA: as many as fit it, but no more than spread the rows over
+// all SMs, and one named barrier each (15 besides the CTA's own).
+int row_groups(int64_t rows, int warps, int sms)
+{
+    const int64_t fit = std::min(kRowThreadsMax / 32 / warps, warps == 1 ? 16 : 15), spread = (rows + sms - 1) / sms;
+    return static_cast<int>(std::min(fit, spread));
+}
 
 template <typename T>
 const void *norm_kernel(int nv, bool staged)
 {
-    return nv == 1 ? (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 1, true>)
-                             : reinterpret_cast<void *>(&taco_norm_kernel<T, 1, false>))
-                   : (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 2, true>)
-                             : reinterpret_cast<void *>(&taco_norm_kernel<T, 2, false>));
+    return nv == 1   ? (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 1, true>)
+                               : reinterpret_cast<void *>(&taco_norm_kernel<T, 1, false>))
+           : nv == 2 ? (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 2, true>)
+                               : reinterpret_cast<void *>(&taco_norm_kernel<T, 2, false>))
+                     : (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 4, true>)
+                               : reinterpret_cast<void *>(&taco_norm_kernel<T, 4, false>));
+}
+
+// Rows in flight: up to four in the shared memory that the parameters leave.
+int ring_stages(size_t params, size_t stage, int most = 4)
+{
+    while (most > 1 && params + most * stage > kMaxShared)
+        most--;
+    return most;
 }
 
 template <typename T>
 cudaError_t norm_vectors(const NormArgs &a, int sms, cudaStream_t stream)
 {
     NormArgs args = a;
-    const int nv = a.hidden <= 256 ? 1 : 2;
+    const int nv = lane_vectors(a.hidden);
     int warps = static_cast<int>((a.hidden + 256 * nv - 1) / (256 * nv));
-    // As many row groups as fit the CTA, but no more than spread the rows over all SMs; at most 15 barriers.
-    const int64_t fit = std::min(kNormThreads / 32 / warps, warps == 1 ? 32 : 15), spread = (a.rows + sms - 1) / sms;
-    int groups = static_cast<int>(std::min(fit, spread));
+    int groups = row_groups(a.rows, warps, sms);
+    const int threads = warps * groups * 32;
     const int64_t ctas = (a.rows + groups - 1) / groups;
     const bool staged = ctas > sms && (a.weight || a.bias);
-    void *p[] = {&args, &warps, &groups};
-    return launch_kernel(norm_kernel<T>(nv, staged), static_cast<int>(std::min<int64_t>(ctas, sms)), warps * groups * 32,
-                         staged ? 8 * static_cast<size_t>(a.hidden) : 0, stream, p);
+    const size_t params = staged ? 8 * static_cast<size_t>(a.hidden) : 0;
+    const size_t stage = static_cast<size_t>(a.residual ? 2 : 1) * nv * threads * 8 * sizeof(T);
+    int stages = ring_stages(params, stage);
+    void *p[] = {&args, &warps, &groups, &stages};
+    return launch_kernel(norm_kernel<T>(nv, staged), static_cast<int>(std::min<int64_t>(ctas, sms)), threads,
+                         params + stages * stage, stream, p);
 }
 
 template <typename T>
@@ -627,29 +711,27 @@ const void *norm_grad_kernel(int nv, bool records)
                                 : reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 4, false>));
 }
 
-constexpr size_t kMaxShared = 225 * 1024;
-
 template <typename T>
 cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
 {
     const int64_t C = a->hidden;
     if (fits_registers(C)) {
-        const int nv = C <= 256 ? 1 : C <= kGradThreads / 32 * 512 ? 2 : 4;
+        const bool records = !a->x;
+        const int nv = lane_vectors(C);
         int warps = static_cast<int>((C + 256 * nv - 1) / (256 * nv));
-        const int64_t fit = std::min(kGradThreads / 32 / warps, 15), spread = (a->rows + sms - 1) / sms;
-        int groups = static_cast<int>(std::min(fit, spread));
+        int groups = row_groups(a->rows, warps, sms);
         const int threads = warps * groups * 32;
-        const size_t weight = a->weight ? static_cast<size_t>(C * 4 + 15) / 16 * 16 : 0;
-        const size_t stage = static_cast<size_t>(1 + (a->x != nullptr) + (a->dsummed != nullptr)) * nv * threads * 8 * sizeof(T);
-        int stages = 4;
-        while (stages > 1 && weight + stages * stage > kMaxShared)
-            stages--;
+        const size_t weight = a->weight ? static_cast<size_t>(4 * C) : 0;
+        size_t stage = static_cast<size_t>(1 + !records + (a->dsummed != nullptr)) * nv * threads * 8 * sizeof(T);
+        if (records)
+            stage += static_cast<size_t>(groups) * ((C / a->block * (a->block + 8) + 8 + 15) / 16 * 16);
+        int stages = ring_stages(weight, stage);
         const size_t smem = weight + std::max<size_t>(stages * stage, groups > 1 ? 8 * static_cast<size_t>(C) : 0);
-        if (smem <= kMaxShared) {
+        if (smem <= kMaxShared && (!records || stages >= 3)) {
             a->nparts = static_cast<int>(std::min({(a->rows + groups - 1) / groups, static_cast<int64_t>(sms),
                                                    static_cast<int64_t>(kMaxColumnParts)}));
             void *p[] = {a, &warps, &groups, &stages};
-            return launch_kernel(norm_grad_kernel<T>(nv, !a->x), a->nparts, threads, smem, stream, p);
+            return launch_kernel(norm_grad_kernel<T>(nv, records), a->nparts, threads, smem, stream, p);
         }
     }
     void *p[] = {a};
@@ -664,13 +746,14 @@ cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
 template <typename T>
 cudaError_t init_norm_type()
 {
-    cudaError_t e = cudaSuccess;
-    for (int nv = 1; nv <= 2 && e == cudaSuccess; nv++)
-        e = cudaFuncSetAttribute(norm_kernel<T>(nv, true), cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kMaxVectorWidth);
-    for (int i = 0; i < 6 && e == cudaSuccess; i++)
-        e = cudaFuncSetAttribute(norm_grad_kernel<T>(1 << i / 2, i % 2 != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kMaxShared));
-    return e;
+    for (int nv = 1; nv <= 4; nv *= 2)
+        for (int i = 0; i < 4; i++) {
+            const cudaError_t e = cudaFuncSetAttribute(i < 2 ? norm_kernel<T>(nv, i != 0) : norm_grad_kernel<T>(nv, i != 2),
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxShared));
+            if (e != cudaSuccess)
+                return e;
+        }
+    return cudaSuccess;
 }
 
 }  // namespace

@@ -114,6 +114,36 @@ __device__ __forceinline__ Raw8<__half> pack8(const float (&f)[8], const __half 
     return r;
 }
 
+// Eight values as four pairs, for packed binary32 arithmetic.
+struct F8 {
+    float2 v[4];
+};
+
+template <typename T>
+__device__ __forceinline__ F8 unpack(const Raw8<T> &r)
+{
+    float f[8];
+    unpack8(r, f);
+    return F8{{make_float2(f[0], f[1]), make_float2(f[2], f[3]), make_float2(f[4], f[5]), make_float2(f[6], f[7])}};
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> pack(const F8 &x)
+{
+    const float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+    return pack8(f, static_cast<const T *>(nullptr));
+}
+
+template <typename T>
+__device__ __forceinline__ void store_raw8(T *p, const Raw8<T> &r)
+{
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); i++)
+        reinterpret_cast<uint4 *>(p)[i] = r.v[i];
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Rounds to T and stores eight consecutive elements.
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float (&f)[8])
@@ -202,8 +232,9 @@ __device__ __forceinline__ float2 codes2_to_float2(uint32_t pair, int code)
 }
 
 // Eight code bytes as floats.
-__device__ __forceinline__ void codes8_to_float(uint2 c, int code, float (&f)[8])
+__device__ __forceinline__ F8 codes8_to_float(uint2 c, int code)
 {
+    F8 f;
     const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -217,8 +248,10 @@ __device__ __forceinline__ void codes8_to_float(uint2 c, int code, float (&f)[8]
             a = e5m2x2_to_float2(w[h] & 0xffffu);
             b = e5m2x2_to_float2(w[h] >> 16);
         }
-        f[4 * h] = a.x, f[4 * h + 1] = a.y, f[4 * h + 2] = b.x, f[4 * h + 3] = b.y;
+        f.v[2 * h] = a;
+        f.v[2 * h + 1] = b;
     }
+    return f;
 }
 
 // Factor s / alpha of a record's (alpha, s).
@@ -228,55 +261,56 @@ __device__ __forceinline__ float meta_factor(uint2 m)
     return alpha == 1.f ? s : __fdiv_rn(s, alpha);
 }
 
-__device__ __forceinline__ uint32_t max_abs_bits8(const float (&f)[8])
+// The scale of the block that this lane's eight values belong to and their
+// codes.  A warp's vector holds 256 consecutive elements, lane l those from 8 l
+// on, so a block of B <= 256 lies in B / 8 neighbouring lanes; a block of 512 is
+// the two vectors of a pair, whose maxima the caller joins.
+__device__ __forceinline__ uint32_t block_max(const F8 &u, int block)
 {
-    uint32_t m = 0;
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-        m = max(m, abs_bits(f[i]));
-    return m;
+    for (int i = 0; i < 4; i++)
+        top = max(top, max(abs_bits(u.v[i].x), abs_bits(u.v[i].y)));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+        if (8 * d < block)
+            top = max(top, __shfl_xor_sync(kFullMask, top, d));
+    return top;
 }
 
-// Writes the records of NV vectors of eight values a lane.  Vector j of a warp
-// holds 256 consecutive elements, lane l those from 8 l on, so a block of B <=
-// 256 lies in B / 8 neighbouring lanes of one vector and a block of 512 in a
-// pair of vectors (an even j and j + 1).  at[j] is the first code's address; a
-// lane whose at[j] is null takes no part (whole blocks only).
-template <int NV>
-__device__ __forceinline__ void write_records(const float (&u)[NV][8], uint8_t *const (&at)[NV], int block, int code)
+// Writes this lane's codes to `at` and, from the lane that holds the block's
+// last ones, (1, s) behind them.  `from`: first element's place in the block.
+__device__ __forceinline__ void write_codes(const F8 &u, uint32_t top, uint8_t *at, int from, int block, int code)
 {
-    const int lane = threadIdx.x & 31;
+    float inv;
+    const float s = record_scale(top, code, &inv);
+    uint2 q = make_uint2(0u, 0u);
+    if (inv != 0.f)
+        q = make_uint2(encode4_scaled(code, u.v[0], u.v[1], inv), encode4_scaled(code, u.v[2], u.v[3], inv));
+    *reinterpret_cast<uint2 *>(at) = q;
+    if (from + 8 == block)
+        *reinterpret_cast<float2 *>(at + 8) = make_float2(1.f, s);
+}
+
+// Records of NV vectors of eight a lane, vector j starting at column col[j] of a
+// row of C; `row` is the row's first record byte.
+template <int NV>
+__device__ __forceinline__ void write_records(const F8 (&u)[NV], const int (&col)[NV], int C, uint8_t *row, int block, int code)
+{
     uint32_t top[NV];
 #pragma unroll
-    for (int j = 0; j < NV; j++) {
-        top[j] = max_abs_bits8(u[j]);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-            if (8 * d < block)
-                top[j] = max(top[j], __shfl_xor_sync(kFullMask, top[j], d));
-    }
+    for (int j = 0; j < NV; j++)
+        top[j] = block_max(u[j], block);
     if (NV > 1 && block == 512) {
 #pragma unroll
         for (int j = 0; j + 1 < NV; j += 2)
             top[j] = top[j + 1] = max(top[j], top[j + 1]);
     }
+    const int shift = 31 - __clz(block);
 #pragma unroll
-    for (int j = 0; j < NV; j++) {
-        float inv;
-        const float s = record_scale(top[j], code, &inv);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            v[i] = inv == 0.f ? 0.f : __fmul_rn(u[j][i], inv);
-        const uint2 q = make_uint2(encode4(code, v[0], v[1], v[2], v[3]), encode4(code, v[4], v[5], v[6], v[7]));
-        if (at[j]) {
-            *reinterpret_cast<uint2 *>(at[j]) = q;
-            // the lane that holds the block's last codes writes (alpha, s) behind them
-            const int from = lane * 8 + (block == 512 ? (j & 1) * 256 : 0);
-            if ((from & (block - 1)) + 8 == block)
-                *reinterpret_cast<float2 *>(at[j] + 8) = make_float2(1.f, s);
-        }
-    }
+    for (int j = 0; j < NV; j++)
+        if (col[j] < C)
+            write_codes(u[j], top[j], row + col[j] + (col[j] >> shift) * 8, col[j] & (block - 1), block, code);
 }
 
 // Byte of element `col` in a record row.
