@@ -102,7 +102,7 @@ __device__ __forceinline__ float inv_sqrt(float v)
     return v > 0.f && v < 3.0e38f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
-constexpr int kRowThreadsMax = 512;
+constexpr int kNormThreads = 768, kGradThreads = 512;   // the backward pass keeps 64 column sums a thread
 
 // Rows come to shared memory `stages` rows ahead by cp.async, 16 bytes at a
 // time.  Each thread copies exactly the pieces of x, dy and the like that it
@@ -133,17 +133,27 @@ __device__ __forceinline__ void copies_landed(int ahead)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Eight binary32 values in shared memory.
-__device__ __forceinline__ F8 load_shared8(const float *p)
+// Parameters in shared memory: of every eight the first four in one plane of
+// C / 2 floats and the others in the next, so that a warp's 16-byte reads are
+// consecutive (read 32 bytes apart, they would take the banks twice).
+__device__ __forceinline__ F8 load_plane8(const float *p, int c, int C)
 {
-    return unpack(Raw8<float>{{*reinterpret_cast<const uint4 *>(p), *reinterpret_cast<const uint4 *>(p + 4)}});
+    return unpack(Raw8<float>{{*reinterpret_cast<const uint4 *>(p + c / 2), *reinterpret_cast<const uint4 *>(p + C / 2 + c / 2)}});
+}
+
+__device__ __forceinline__ void stage_param8(float *p, const void *from, int dtype, int c, int C)
+{
+    float f[8];
+    load_param8(from, dtype, c, f);
+    *reinterpret_cast<float4 *>(p + c / 2) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4 *>(p + C / 2 + c / 2) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
 // A row's columns over a group of `warps` warps: vector j (of NV) of warp w
 // starts at column 256 (w NV + j), lane l holds eight columns from 8 l on.  The
 // CTA's groups work on rows of their own.  Many columns a thread keep the two
-// row sums cheap: 32 a thread run 8192 x 4096 bf16 in REPLACE_FWD, eight a thread
-// (twice the warps, two rows a pass) in 51 us.
+// row sums cheap: 32 a thread run 8192 x 4096 bf16 with a residual in 47 us, eight a thread
+// (twice the warps, two rows a pass) in 58 us.
 //
 // Statistics with one barrier: each warp sums its values and then their squared
 // distances from its own mean p_w = S_w / n_w; with the row's mean m the sum of
@@ -152,11 +162,13 @@ __device__ __forceinline__ F8 load_shared8(const float *p)
 //
 // weight and bias stay in shared memory (STAGED) where a CTA has several rows
 // to read them for.
-template <typename T, int NV, bool STAGED>
-__global__ void __launch_bounds__(kRowThreadsMax, 1) taco_norm_kernel(NormArgs a, int warps, int groups, int stages)
+// FULL: every lane's every vector lies inside the row, so nothing branches
+// between the loads.
+template <typename T, int NV, bool STAGED, bool FULL>
+__global__ void __launch_bounds__(kNormThreads, 1) taco_norm_kernel(NormArgs a, int warps, int groups, int stages)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // weight, bias (STAGED), then the copies
-    __shared__ float2 sums[2][16];
+    __shared__ float2 sums[2][32];
     grid_launch_dependents();
     constexpr int kUnits = sizeof(T) / 2;                 // 16-byte units of eight elements
     const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kRowThreadsMax, 1) taco_norm_kernel(NormArgs a
                 for (int j = 0; j < NV; j++)
 #pragma unroll
                     for (int k = 0; k < kUnits; k++, to += unit)
-                        if (col[j] < C)
+                        if (FULL || col[j] < C)
                             copy16(to, reinterpret_cast<const uint4 *>(src + row * C + col[j]) + k);
             };
             piece(x);
@@ -197,21 +209,16 @@ __global__ void __launch_bounds__(kRowThreadsMax, 1) taco_norm_kernel(NormArgs a
         copy_row(first + i * step, i);
     if (STAGED) {
         for (int c = threadIdx.x * 8; c < C; c += blockDim.x * 8) {
-            float f[8];
-            if (a.weight) {
-                load_param8(a.weight, a.param_dtype, c, f);
-                store8(sparam + c, f);
-            }
-            if (a.bias) {
-                load_param8(a.bias, a.param_dtype, c, f);
-                store8(sparam + C + c, f);
-            }
+            if (a.weight)
+                stage_param8(sparam, a.weight, a.param_dtype, c, C);
+            if (a.bias)
+                stage_param8(sparam + C, a.bias, a.param_dtype, c, C);
         }
         __syncthreads();
     }
     auto param = [&](const void *p, int offset, int c) {
         if (STAGED)
-            return load_shared8(sparam + offset + c);
+            return load_plane8(sparam + offset, c, C);
         float f[8];
         load_param8(p, a.param_dtype, c, f);
         return F8{{make_float2(f[0], f[1]), make_float2(f[2], f[3]), make_float2(f[4], f[5]), make_float2(f[6], f[7])}};
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(kRowThreadsMax, 1) taco_norm_kernel(NormArgs a
         float2 total = both(0.f);
 #pragma unroll
         for (int j = 0; j < NV; j++)
-            if (col[j] < C) {
+            if (FULL || col[j] < C) {
                 Raw8<T> v;
 #pragma unroll
                 for (int k = 0; k < kUnits; k++)
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kRowThreadsMax, 1) taco_norm_kernel(NormArgs a
         float2 squares = both(0.f);
 #pragma unroll
         for (int j = 0; j < NV; j++)
-            if (col[j] < C) {
+            if (FULL || col[j] < C) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const float2 d = add2(h[j].v[i], both(-pivot));
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(kRowThreadsMax, 1) taco_norm_kernel(NormArgs a
         }
 #pragma unroll
         for (int j = 0; j < NV; j++)
-            if (col[j] < C) {
+            if (FULL || col[j] < C) {
                 F8 y;
 #pragma unroll
                 for (int i = 0; i < 4; i++)
@@ -362,12 +369,12 @@ __global__ void __launch_bounds__(kRowThreads) taco_norm_grad_any_kernel(NormGra
 // the one of the row sums of the row before, ahead of which each thread waits
 // for its part of the next row.  A row's place is filled again behind the
 // barrier of the row after it, when every thread has left it.
-template <typename T, int NV, bool RECORDS>
-__global__ void __launch_bounds__(kRowThreadsMax, 1)
+template <typename T, int NV, bool RECORDS, bool FULL>
+__global__ void __launch_bounds__(kGradThreads, 1)
 taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // weight, then the copies
-    __shared__ float2 sums[2][16];
+    __shared__ float2 sums[2][32];
     grid_launch_dependents();
     constexpr int kUnits = sizeof(T) / 2;
     const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
@@ -395,7 +402,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
                 for (int j = 0; j < NV; j++)
 #pragma unroll
                     for (int k = 0; k < kUnits; k++, to += unit)
-                        if (col[j] < C)
+                        if (FULL || col[j] < C)
                             copy16(to, reinterpret_cast<const uint4 *>(static_cast<const T *>(src) + row * C + col[j]) + k);
             };
             piece(a.dy);
@@ -425,11 +432,8 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
         copy_row(first + i * step, i);
     fetch(first);
     if (a.weight) {
-        for (int c = threadIdx.x * 8; c < C; c += blockDim.x * 8) {
-            float f[8];
-            load_param8(a.weight, a.param_dtype, c, f);
-            store8(sweight + c, f);
-        }
+        for (int c = threadIdx.x * 8; c < C; c += blockDim.x * 8)
+            stage_param8(sweight, a.weight, a.param_dtype, c, C);
     }
     if (RECORDS)
         copies_landed(stages - 2);
@@ -481,7 +485,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
         auto weighted = [&](int j, const F8 &g) {
             if (!a.weight)
                 return g;
-            F8 f = load_shared8(sweight + col[j]);
+            F8 f = load_plane8(sweight, col[j], C);
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 f.v[i] = mul2(f.v[i], g.v[i]);
@@ -490,7 +494,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
         float2 t1 = both(0.f), t2 = both(0.f);
 #pragma unroll
         for (int j = 0; j < NV; j++)
-            if (col[j] < C) {
+            if (FULL || col[j] < C) {
                 const F8 w = weighted(j, vector(0, j)), xh = normalised(j);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -529,7 +533,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
         const float c1 = s1 * inv_c, c2 = s2 * inv_c;
 #pragma unroll
         for (int j = 0; j < NV; j++)
-            if (col[j] < C) {
+            if (FULL || col[j] < C) {
                 const F8 g = vector(0, j), xh = normalised(j);
                 F8 w = weighted(j, g);
 #pragma unroll
@@ -557,7 +561,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
         if (g == group) {
 #pragma unroll
             for (int j = 0; j < NV; j++)
-                if (col[j] < C) {
+                if (FULL || col[j] < C) {
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         float2 *w = acc + i * (C / 8) + col[j] / 8, *b = w + C / 2;
@@ -646,21 +650,25 @@ int lane_vectors(int64_t hidden) { return hidden <= 256 ? 1 : hidden <= 512 ? 2 
 
 // Row groups of a CTA: as many as fit it, but no more than spread the rows over
 // all SMs, and one named barrier each (15 besides the CTA's own).
-int row_groups(int64_t rows, int warps, int sms)
+int row_groups(int64_t rows, int warps, int threads, int sms)
 {
-    const int64_t fit = std::min(kRowThreadsMax / 32 / warps, warps == 1 ? 16 : 15), spread = (rows + sms - 1) / sms;
+    const int64_t fit = std::min(threads / 32 / warps, warps == 1 ? 32 : 15), spread = (rows + sms - 1) / sms;
     return static_cast<int>(std::min(fit, spread));
 }
 
-template <typename T>
-const void *norm_kernel(int nv, bool staged)
+template <typename T, bool FLAG>
+const void *norm_kernel(int nv, bool full)
 {
-    return nv == 1   ? (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 1, true>)
-                               : reinterpret_cast<void *>(&taco_norm_kernel<T, 1, false>))
-           : nv == 2 ? (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 2, true>)
-                               : reinterpret_cast<void *>(&taco_norm_kernel<T, 2, false>))
-                     : (staged ? reinterpret_cast<void *>(&taco_norm_kernel<T, 4, true>)
-                               : reinterpret_cast<void *>(&taco_norm_kernel<T, 4, false>));
+    return nv == 1   ? reinterpret_cast<void *>(&taco_norm_kernel<T, 1, FLAG, false>)
+           : nv == 2 ? reinterpret_cast<void *>(&taco_norm_kernel<T, 2, FLAG, false>)
+           : full    ? reinterpret_cast<void *>(&taco_norm_kernel<T, 4, FLAG, true>)
+                     : reinterpret_cast<void *>(&taco_norm_kernel<T, 4, FLAG, false>);
+}
+
+template <typename T>
+const void *norm_kernel(int nv, bool staged, bool full)
+{
+    return staged ? norm_kernel<T, true>(nv, full) : norm_kernel<T, false>(nv, full);
 }
 
 // Rows in flight: up to four in the shared memory that the parameters leave.
@@ -677,7 +685,7 @@ cudaError_t norm_vectors(const NormArgs &a, int sms, cudaStream_t stream)
     NormArgs args = a;
     const int nv = lane_vectors(a.hidden);
     int warps = static_cast<int>((a.hidden + 256 * nv - 1) / (256 * nv));
-    int groups = row_groups(a.rows, warps, sms);
+    int groups = row_groups(a.rows, warps, kNormThreads, sms);
     const int threads = warps * groups * 32;
     const int64_t ctas = (a.rows + groups - 1) / groups;
     const bool staged = ctas > sms && (a.weight || a.bias);
@@ -685,7 +693,7 @@ cudaError_t norm_vectors(const NormArgs &a, int sms, cudaStream_t stream)
     const size_t stage = static_cast<size_t>(a.residual ? 2 : 1) * nv * threads * 8 * sizeof(T);
     int stages = ring_stages(params, stage);
     void *p[] = {&args, &warps, &groups, &stages};
-    return launch_kernel(norm_kernel<T>(nv, staged), static_cast<int>(std::min<int64_t>(ctas, sms)), threads,
+    return launch_kernel(norm_kernel<T>(nv, staged, a.hidden == warps * nv * 256), static_cast<int>(std::min<int64_t>(ctas, sms)), threads,
                          params + stages * stage, stream, p);
 }
 
@@ -700,15 +708,19 @@ cudaError_t norm_any(const NormArgs &a, int sms, cudaStream_t stream)
                          stream, p);
 }
 
-template <typename T>
-const void *norm_grad_kernel(int nv, bool records)
+template <typename T, bool FLAG>
+const void *norm_grad_kernel(int nv, bool full)
 {
-    return nv == 1   ? (records ? reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 1, true>)
-                                : reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 1, false>))
-           : nv == 2 ? (records ? reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 2, true>)
-                                : reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 2, false>))
-                     : (records ? reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 4, true>)
-                                : reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 4, false>));
+    return nv == 1   ? reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 1, FLAG, false>)
+           : nv == 2 ? reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 2, FLAG, false>)
+           : full    ? reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 4, FLAG, true>)
+                     : reinterpret_cast<void *>(&taco_norm_grad_kernel<T, 4, FLAG, false>);
+}
+
+template <typename T>
+const void *norm_grad_kernel(int nv, bool records, bool full)
+{
+    return records ? norm_grad_kernel<T, true>(nv, full) : norm_grad_kernel<T, false>(nv, full);
 }
 
 template <typename T>
@@ -719,7 +731,7 @@ cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
         const bool records = !a->x;
         const int nv = lane_vectors(C);
         int warps = static_cast<int>((C + 256 * nv - 1) / (256 * nv));
-        int groups = row_groups(a->rows, warps, sms);
+        int groups = row_groups(a->rows, warps, kGradThreads, sms);
         const int threads = warps * groups * 32;
         const size_t weight = a->weight ? static_cast<size_t>(4 * C) : 0;
         size_t stage = static_cast<size_t>(1 + !records + (a->dsummed != nullptr)) * nv * threads * 8 * sizeof(T);
@@ -731,7 +743,7 @@ cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
             a->nparts = static_cast<int>(std::min({(a->rows + groups - 1) / groups, static_cast<int64_t>(sms),
                                                    static_cast<int64_t>(kMaxColumnParts)}));
             void *p[] = {a, &warps, &groups, &stages};
-            return launch_kernel(norm_grad_kernel<T>(nv, records), a->nparts, threads, smem, stream, p);
+            return launch_kernel(norm_grad_kernel<T>(nv, records, C == warps * nv * 256), a->nparts, threads, smem, stream, p);
         }
     }
     void *p[] = {a};
@@ -747,8 +759,9 @@ template <typename T>
 cudaError_t init_norm_type()
 {
     for (int nv = 1; nv <= 4; nv *= 2)
-        for (int i = 0; i < 4; i++) {
-            const cudaError_t e = cudaFuncSetAttribute(i < 2 ? norm_kernel<T>(nv, i != 0) : norm_grad_kernel<T>(nv, i != 2),
+        for (int i = 0; i < 8; i++) {
+            const bool flag = i & 1, full = i & 2;
+            const cudaError_t e = cudaFuncSetAttribute(i < 4 ? norm_kernel<T>(nv, flag, full) : norm_grad_kernel<T>(nv, flag, full),
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxShared));
             if (e != cudaSuccess)
                 return e;
