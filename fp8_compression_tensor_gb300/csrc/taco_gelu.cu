@@ -8,6 +8,9 @@
 // Backward, with u decoded from the records: dx = dy (Phi(u) + u phi(u)), or
 // the tanh form's slope; dbias = sum over rows of dx; y again when the next
 // weight gradient needs it.
+#include <algorithm>
+#include <climits>
+
 #include "taco_kernels.h"
 #include "taco_train.cuh"
 
@@ -15,111 +18,263 @@ namespace taco {
 namespace {
 
 constexpr float kTanhA = 0.7978845608028654f, kTanhB = 0.044715f;
-constexpr float kSqrtHalf = 0.7071067811865476f, kInvSqrt2Pi = 0.3989422804014327f;
+constexpr float kLog2e = 1.4426950408889634f, kInvSqrt2Pi = 0.3989422804014327f;
 
-// Phi(u) from the complementary error function: no cancellation for negative u.
-__device__ __forceinline__ float normal_cdf(float u) { return 0.5f * erfcf(-kSqrtHalf * u); }
-
-__device__ __forceinline__ float gelu_value(float u, int tanh_form)
+__device__ __forceinline__ float exp2_fast(float v)
 {
-    if (tanh_form)
-        return 0.5f * u * (1.f + tanhf(kTanhA * (u + kTanhB * u * u * u)));
-    return u * normal_cdf(u);
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-__device__ __forceinline__ float gelu_slope(float u, int tanh_form)
+__device__ __forceinline__ float reciprocal_fast(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The normal distribution function of a pair, and E = exp(-u^2 / 2).  With
+// a = |u| the upper tail 1 - Phi(a) = erfc(a / sqrt 2) / 2 equals E t Q(t), t =
+// 1 / (1 + 0.3 a): erfc(z) exp(z^2) is smooth and falls like 1/z, so a
+// polynomial in t follows it on the whole half line.  Q (degree 7) is a
+// least-squares fit reweighted towards the smallest largest relative error on
+// 0 <= a <= 14, 1.5e-7; in binary32 the tail is off by at most 2.5e-7.  Negative
+// u take the tail itself, so nothing cancels.  One exponential and one reciprocal
+// serve Phi and, in the gradient, the density too.
+__device__ __forceinline__ float2 normal_cdf2(float2 u, float2 &e)
+{
+    const float2 half = make_float2(-0.5f * kLog2e, -0.5f * kLog2e);
+    const float2 x = mul2(mul2(u, u), half);
+    e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+    const float2 d = fma2(make_float2(fabsf(u.x), fabsf(u.y)), both(0.3f), both(1.f));
+    const float2 t = make_float2(reciprocal_fast(d.x), reciprocal_fast(d.y));
+    float2 q = both(0.03567478060722351f);
+    q = fma2(q, t, both(-0.1572030931711197f));
+    q = fma2(q, t, both(0.20635348558425903f));
+    q = fma2(q, t, both(-0.05368363484740257f));
+    q = fma2(q, t, both(0.1285616159439087f));
+    q = fma2(q, t, both(0.09991350024938583f));
+    q = fma2(q, t, both(0.12075395882129669f));
+    q = fma2(q, t, both(0.11962930113077164f));
+    q = mul2(mul2(q, t), e);
+    return make_float2(u.x < 0.f ? q.x : 1.f - q.x, u.y < 0.f ? q.y : 1.f - q.y);
+}
+
+// 1 / (1 + exp(-2 v)) = (1 + tanh v) / 2 for v = a (u + b u^3).
+__device__ __forceinline__ float2 tanh_gate2(float2 u)
+{
+    const float2 poly = fma2(mul2(u, u), both(kTanhA * kTanhB), both(kTanhA));
+    const float2 x = mul2(mul2(poly, u), both(-2.f * kLog2e));
+    return make_float2(reciprocal_fast(1.f + exp2_fast(x.x)), reciprocal_fast(1.f + exp2_fast(x.y)));
+}
+
+__device__ __forceinline__ float2 gelu_value2(float2 u, int tanh_form)
+{
+    float2 e;
+    return mul2(u, tanh_form ? tanh_gate2(u) : normal_cdf2(u, e));
+}
+
+// gelu(u) and its slope.
+__device__ __forceinline__ void gelu_both2(float2 u, int tanh_form, float2 &y, float2 &slope)
 {
     if (tanh_form) {
-        const float t = tanhf(kTanhA * (u + kTanhB * u * u * u));
-        return 0.5f * (1.f + t) + 0.5f * u * (1.f - t * t) * kTanhA * (1.f + 3.f * kTanhB * u * u);
+        const float2 g = tanh_gate2(u);
+        // Beyond |u| = 16 the gate is 0 or 1 and its slope 0; the clamp keeps u^2 finite.
+        const float2 c = make_float2(fminf(fmaxf(u.x, -16.f), 16.f), fminf(fmaxf(u.y, -16.f), 16.f));
+        const float2 inner = fma2(mul2(c, c), both(6.f * kTanhA * kTanhB), both(2.f * kTanhA));
+        const float2 rest = fma2(g, make_float2(-g.x, -g.y), g);          // g (1 - g)
+        slope = fma2(mul2(c, inner), rest, g);
+        // A NaN does not pass the clamp.
+        if (u.x != u.x)
+            slope.x = u.x;
+        if (u.y != u.y)
+            slope.y = u.y;
+        y = mul2(u, g);
+    } else {
+        float2 e;
+        const float2 cdf = normal_cdf2(u, e);
+        slope = fma2(mul2(u, both(kInvSqrt2Pi)), e, cdf);
+        y = mul2(u, cdf);
     }
-    return normal_cdf(u) + u * kInvSqrt2Pi * expf(-0.5f * u * u);
 }
 
-// A warp per block of B elements (without records: any pieces of B elements, the last one ragged).
+// Whole vectors of eight: a warp takes 512 consecutive elements at a time, two
+// vectors a lane (the layout of block_max), with the next ones' loads in flight.
 template <typename T>
-__global__ void __launch_bounds__(256) taco_gelu_kernel(GeluArgs a)
+__global__ void __launch_bounds__(256, 3) taco_gelu_kernel(GeluArgs a)
 {
     grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t n = a.rows * a.hidden, step = static_cast<int64_t>(gridDim.x) * 8 * 512;
+    int64_t at = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 512 + lane * 8;
+    const T *x = static_cast<const T *>(a.x);
+    // Column of the first vector, kept up by adding the step modulo the width.
+    const int C = static_cast<int>(a.hidden), col_step = static_cast<int>(step % C), col_next = 256 % C;
+    int col = static_cast<int>(at % C);
+    const int shift = a.packed ? 31 - __clz(a.block) : 0;
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, B = a.block;
-    const int64_t n = a.rows * a.hidden, blocks = (n + B - 1) / B;
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); k < blocks; k += 8ll * gridDim.x) {
-        const int len = static_cast<int>(n - k * B < B ? n - k * B : B);
-        float u[16];
-        uint32_t top = 0;
+    Raw8<T> next[2];
+    auto fetch = [&](int64_t i) {
 #pragma unroll
-        for (int j = 0; j < 16; j++) {
-            const int i = lane + 32 * j;
-            if (i < len) {
-                u[j] = to_float(static_cast<const T *>(a.x)[k * B + i]);
-                if (a.bias)
-                    u[j] += load_param(a.bias, a.param_dtype, (k * B + i) % a.hidden);
-                top = max(top, abs_bits(u[j]));
+        for (int j = 0; j < 2; j++)
+            if (i + 256 * j < n)
+                next[j] = load_raw8(x + i + 256 * j);
+    };
+    fetch(at);
+    // Every lane of a warp that has work goes round together.
+    for (; at - lane * 8 < n; at += step) {
+        F8 u[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            u[j] = unpack(next[j]);
+        fetch(at + step);
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                int c = col + j * col_next;
+                c = c >= C ? c - C : c;
+                const F8 b = load_param_f8(a.bias, a.param_dtype, c);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    u[j].v[i] = add2(u[j].v[i], b.v[i]);
             }
         }
-        float inv = 0.f, s = 0.f;
-        uint8_t *rec = a.packed + k * (B + 8);
+        col += col_step;
+        col = col >= C ? col - C : col;
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            if (at + 256 * j < n) {
+                F8 y;
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    y.v[i] = gelu_value2(u[j].v[i], a.tanh_form);
+                store_raw8(static_cast<T *>(a.y) + at + 256 * j, pack<T>(y));
+            }
         if (a.packed) {
-            top = __reduce_max_sync(kFullMask, top);
-            s = record_scale(top, a.code, &inv);
-            if (lane == 0)
-                *reinterpret_cast<float2 *>(rec + B) = make_float2(1.f, s);
-        }
+            uint32_t top[2] = {block_max(u[0], a.block), block_max(u[1], a.block)};
+            if (a.block == 512)
+                top[0] = top[1] = max(top[0], top[1]);
 #pragma unroll
-        for (int j = 0; j < 16; j++) {
-            const int i = lane + 32 * j;
-            if (i < len) {
-                static_cast<T *>(a.y)[k * B + i] = from_float<T>(gelu_value(u[j], a.tanh_form));
-                if (a.packed)
-                    rec[i] = record_code(u[j], inv, a.code);
+            for (int j = 0; j < 2; j++) {
+                const int64_t i = at + 256 * j;
+                if (i < n)
+                    write_codes(u[j], top[j], a.packed + i + (i >> shift) * 8, static_cast<int>(i & (a.block - 1)), a.block, a.code);
             }
         }
     }
 }
 
-// A thread per column, rows part, part + nparts, ...
+// Widths that are no multiple of 8 (no records then): element by element.
 template <typename T>
-__global__ void __launch_bounds__(128) taco_gelu_grad_kernel(GeluGradArgs a)
+__global__ void __launch_bounds__(256) taco_gelu_any_kernel(GeluArgs a)
 {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int64_t C = a.hidden, c = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-    if (c >= C)
-        return;
-    float db = 0.f;
-    for (int64_t row = blockIdx.y; row < a.rows; row += a.nparts) {
-        const int64_t i = row * C + c;
-        const float u = record_value(a.packed, i, a.block, a.code);
-        const float d = to_float(static_cast<const T *>(a.dy)[i]) * gelu_slope(u, a.tanh_form);
-        static_cast<T *>(a.dx)[i] = from_float<T>(d);
-        if (a.y)
-            static_cast<T *>(a.y)[i] = from_float<T>(gelu_value(u, a.tanh_form));
-        db += d;
+    const int64_t n = a.rows * a.hidden;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += 256ll * gridDim.x) {
+        float u = to_float(static_cast<const T *>(a.x)[i]);
+        if (a.bias)
+            u += load_param(a.bias, a.param_dtype, i % a.hidden);
+        static_cast<T *>(a.y)[i] = from_float<T>(gelu_value2(make_float2(u, u), a.tanh_form).x);
     }
-    if (a.parts)
-        a.parts[static_cast<int64_t>(blockIdx.y) * C + c] = db;
+}
+
+// Gradient: a CTA takes a strip of `strip` vectors of eight columns (at most 32,
+// strips of even size), a thread one of them in every 512 / strip-th row, so the
+// bias gradient stays in its registers; the CTA's rows are added in order at the
+// end.  The next row's loads are in flight.
+constexpr int kGradThreads = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGradArgs a, int strip)
+{
+    __shared__ float part[kGradThreads * 8];
+    grid_launch_dependents();
+    const int rows_a_pass = kGradThreads / strip, mine = threadIdx.x / strip, lane = threadIdx.x - mine * strip;
+    const int64_t C = a.hidden, col = (static_cast<int64_t>(blockIdx.x) * strip + lane) * 8;
+    const bool in = mine < rows_a_pass && col < C;
+    const int64_t step = static_cast<int64_t>(gridDim.y) * rows_a_pass;
+    const int64_t block = col / a.block, pitch = C / a.block * (a.block + 8);
+    const uint8_t *rec = a.packed + block * (a.block + 8);
+    const int within = static_cast<int>(col - block * a.block);
+    grid_dependency_wait();
+    F8 db;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        db.v[i] = both(0.f);
+    Raw8<T> next_dy;
+    uint2 next_codes = {}, next_meta = {};
+    auto fetch = [&](int64_t row) {
+        if (in && row < a.rows) {
+            next_dy = load_raw8(static_cast<const T *>(a.dy) + row * C + col);
+            next_codes = __ldg(reinterpret_cast<const uint2 *>(rec + row * pitch + within));
+            next_meta = __ldg(reinterpret_cast<const uint2 *>(rec + row * pitch + a.block));
+        }
+    };
+    int64_t row = static_cast<int64_t>(blockIdx.y) * rows_a_pass + mine;
+    fetch(row);
+    if (in)
+        for (; row < a.rows; row += step) {
+            const F8 g = unpack(next_dy), q = codes8_to_float(next_codes, a.code);
+            const float s = meta_factor(next_meta);
+            fetch(row + step);
+            F8 d, y;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float2 slope;
+                gelu_both2(mul2(q.v[i], both(s)), a.tanh_form, y.v[i], slope);
+                d.v[i] = mul2(g.v[i], slope);
+                db.v[i] = add2(db.v[i], d.v[i]);
+            }
+            store_raw8(static_cast<T *>(a.dx) + row * C + col, pack<T>(d));
+            if (a.y)
+                store_raw8(static_cast<T *>(a.y) + row * C + col, pack<T>(y));
+        }
+    if (!a.parts)
+        return;
+    // Sums of the rows that the CTA's threads took, column by column.
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        part[2 * i * kGradThreads + threadIdx.x] = db.v[i].x;
+        part[(2 * i + 1) * kGradThreads + threadIdx.x] = db.v[i].y;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < strip * 8; c += kGradThreads) {
+        const int64_t column = static_cast<int64_t>(blockIdx.x) * strip * 8 + c;
+        if (column >= C)
+            break;
+        float sum = 0.f;
+        for (int r = 0; r < rows_a_pass; r++)
+            sum += part[(c & 7) * kGradThreads + r * strip + (c >> 3)];
+        a.parts[static_cast<int64_t>(blockIdx.y) * C + column] = sum;
+    }
 }
 
 template <typename T>
 cudaError_t gelu(const GeluArgs &a, int sms, cudaStream_t stream)
 {
     GeluArgs args = a;
-    if (!a.packed)
-        args.block = 512;
     void *p[] = {&args};
-    const int64_t want = (a.rows * a.hidden + 8ll * args.block - 1) / (8ll * args.block), cap = static_cast<int64_t>(sms) * 32;
-    return launch_kernel(reinterpret_cast<void *>(&taco_gelu_kernel<T>), static_cast<int>(want < cap ? want : cap), 256,
-                         0, stream, p);
+    const int64_t n = a.rows * a.hidden;
+    if (a.hidden % 8 || a.hidden > INT32_MAX / 2) {
+        const int64_t want = (n + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
+        return launch_kernel(reinterpret_cast<void *>(&taco_gelu_any_kernel<T>), static_cast<int>(std::min(want, cap)), 256, 0, stream, p);
+    }
+    const int64_t want = (n + 4095) / 4096, cap = static_cast<int64_t>(sms) * 3;
+    return launch_kernel(reinterpret_cast<void *>(&taco_gelu_kernel<T>), static_cast<int>(std::min(want, cap)), 256, 0, stream, p);
 }
 
 template <typename T>
-cudaError_t gelu_grad(const GeluGradArgs &a, int, cudaStream_t stream)
+cudaError_t gelu_grad(GeluGradArgs *a, int sms, cudaStream_t stream)
 {
-    GeluGradArgs args = a;
-    void *p[] = {&args};
-    return launch_kernel_2d(reinterpret_cast<void *>(&taco_gelu_grad_kernel<T>),
-                            static_cast<unsigned>((a.hidden + 127) / 128), static_cast<unsigned>(a.nparts), 128, 0, stream, p);
+    const int64_t vectors = a->hidden / 8, strips = (vectors + 31) / 32;
+    int strip = static_cast<int>((vectors + strips - 1) / strips);
+    const int64_t rows_a_pass = kGradThreads / strip, passes = (a->rows + rows_a_pass - 1) / rows_a_pass;
+    a->nparts = static_cast<int>(std::min<int64_t>({passes, std::max<int64_t>(1, 2 * sms / strips), kMaxColumnParts}));
+    void *p[] = {a, &strip};
+    return launch_kernel_2d(reinterpret_cast<void *>(&taco_gelu_grad_kernel<T>), static_cast<unsigned>(strips),
+                            static_cast<unsigned>(a->nparts), kGradThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -133,9 +288,9 @@ cudaError_t launch_gelu(int dtype, const GeluArgs &a, int sms, cudaStream_t stre
 
 cudaError_t launch_gelu_grad(int dtype, GeluGradArgs *a, int sms, cudaStream_t stream)
 {
-    return dtype == kTypeBf16  ? gelu_grad<__nv_bfloat16>(*a, sms, stream)
-           : dtype == kTypeF16 ? gelu_grad<__half>(*a, sms, stream)
-                               : gelu_grad<float>(*a, sms, stream);
+    return dtype == kTypeBf16  ? gelu_grad<__nv_bfloat16>(a, sms, stream)
+           : dtype == kTypeF16 ? gelu_grad<__half>(a, sms, stream)
+                               : gelu_grad<float>(a, sms, stream);
 }
 
 }  // namespace taco

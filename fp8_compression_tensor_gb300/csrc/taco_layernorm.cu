@@ -219,9 +219,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) taco_norm_kernel(NormArgs a, 
     auto param = [&](const void *p, int offset, int c) {
         if (STAGED)
             return load_plane8(sparam + offset, c, C);
-        float f[8];
-        load_param8(p, a.param_dtype, c, f);
-        return F8{{make_float2(f[0], f[1]), make_float2(f[2], f[3]), make_float2(f[4], f[5]), make_float2(f[6], f[7])}};
+        return load_param_f8(p, a.param_dtype, c);
     };
     int stage = 0, fill = stages - 1;
     uint32_t side = 0;

@@ -165,6 +165,13 @@ __device__ __forceinline__ void load_param8(const void *p, int dtype, int64_t i,
         unpack8(load_raw8(static_cast<const __nv_bfloat16 *>(p) + i), f);
 }
 
+__device__ __forceinline__ F8 load_param_f8(const void *p, int dtype, int64_t i)
+{
+    float f[8];
+    load_param8(p, dtype, i, f);
+    return F8{{make_float2(f[0], f[1]), make_float2(f[2], f[3]), make_float2(f[4], f[5]), make_float2(f[6], f[7])}};
+}
+
 // Value i of a parameter array of run-time type (uniform over the grid).
 __device__ __forceinline__ float load_param(const void *p, int dtype, int64_t i)
 {
