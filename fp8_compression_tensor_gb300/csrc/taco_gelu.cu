@@ -34,20 +34,30 @@ __device__ __forceinline__ float reciprocal_fast(float v)
     return r;
 }
 
-// The normal distribution function of a pair, and E = exp(-u^2 / 2).  With
-// a = |u| the upper tail 1 - Phi(a) = erfc(a / sqrt 2) / 2 equals E t Q(t), t =
-// 1 / (1 + 0.3 a): erfc(z) exp(z^2) is smooth and falls like 1/z, so a
-// polynomial in t follows it on the whole half line.  Q (degree 7) is a
-// least-squares fit reweighted towards the smallest largest relative error on
-// 0 <= a <= 14, 1.5e-7; in binary32 the tail is off by at most 2.5e-7.  Negative
-// u take the tail itself, so nothing cancels.  One exponential and one reciprocal
-// serve Phi and, in the gradient, the density too.
-__device__ __forceinline__ float2 normal_cdf2(float2 u, float2 &e)
+// min(|v|, 30) that keeps a NaN.
+__device__ __forceinline__ float bounded_abs(float v)
 {
-    const float2 half = make_float2(-0.5f * kLog2e, -0.5f * kLog2e);
-    const float2 x = mul2(mul2(u, u), half);
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(v)), "f"(30.f));
+    return r;
+}
+
+// Upper tail q = 1 - Phi(a) of the normal distribution for a = min(|u|, 30), and
+// E = exp(-a^2 / 2) (both are zero in binary32 from a = 14 on, so the bound
+// changes nothing and keeps an infinite u from meeting them).  q = erfc(a / sqrt
+// 2) / 2 equals E t Q(t), t = 1 / (1 + 0.3 a): erfc(z) exp(z^2) is smooth and
+// falls like 1/z, so a polynomial in t follows it on the whole half line.  Q
+// (degree 7) is a least-squares fit reweighted towards the smallest largest
+// relative error on 0 <= a <= 14, 1.5e-7; in binary32 the tail is off by at most
+// 2.5e-7.  One exponential and one reciprocal serve Phi and, in the gradient, the
+// density too.
+//   gelu(u)  = max(u, 0) - a q
+//   gelu'(u) = Phi(u) + u phi(u) = r for u < 0 and 1 - r otherwise, r = q - a phi(a)
+__device__ __forceinline__ float2 normal_tail2(float2 a, float2 &e)
+{
+    const float2 x = mul2(mul2(a, a), both(-0.5f * kLog2e));
     e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-    const float2 d = fma2(make_float2(fabsf(u.x), fabsf(u.y)), both(0.3f), both(1.f));
+    const float2 d = fma2(a, both(0.3f), both(1.f));
     const float2 t = make_float2(reciprocal_fast(d.x), reciprocal_fast(d.y));
     float2 q = both(0.03567478060722351f);
     q = fma2(q, t, both(-0.1572030931711197f));
@@ -57,8 +67,7 @@ __device__ __forceinline__ float2 normal_cdf2(float2 u, float2 &e)
     q = fma2(q, t, both(0.09991350024938583f));
     q = fma2(q, t, both(0.12075395882129669f));
     q = fma2(q, t, both(0.11962930113077164f));
-    q = mul2(mul2(q, t), e);
-    return make_float2(u.x < 0.f ? q.x : 1.f - q.x, u.y < 0.f ? q.y : 1.f - q.y);
+    return mul2(mul2(q, t), e);
 }
 
 // 1 / (1 + exp(-2 v)) = (1 + tanh v) / 2 for v = a (u + b u^3).
@@ -71,8 +80,18 @@ __device__ __forceinline__ float2 tanh_gate2(float2 u)
 
 __device__ __forceinline__ float2 gelu_value2(float2 u, int tanh_form)
 {
+    if (tanh_form)
+        return mul2(u, tanh_gate2(u));
     float2 e;
-    return mul2(u, tanh_form ? tanh_gate2(u) : normal_cdf2(u, e));
+    const float2 a = make_float2(bounded_abs(u.x), bounded_abs(u.y));
+    const float2 q = normal_tail2(a, e);
+    return fma2(make_float2(-a.x, -a.y), q, make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
+}
+
+// v for u >= 0, -v for u < 0.
+__device__ __forceinline__ float with_sign_of(float v, float u)
+{
+    return __uint_as_float(__float_as_uint(v) ^ (__float_as_uint(u) & 0x80000000u));
 }
 
 // gelu(u) and its slope.
@@ -93,16 +112,20 @@ __device__ __forceinline__ void gelu_both2(float2 u, int tanh_form, float2 &y, f
         y = mul2(u, g);
     } else {
         float2 e;
-        const float2 cdf = normal_cdf2(u, e);
-        slope = fma2(mul2(u, both(kInvSqrt2Pi)), e, cdf);
-        y = mul2(u, cdf);
+        const float2 a = make_float2(bounded_abs(u.x), bounded_abs(u.y)), minus = make_float2(-a.x, -a.y);
+        const float2 q = normal_tail2(a, e);
+        const float2 r = fma2(mul2(minus, both(kInvSqrt2Pi)), e, q);
+        // 1/2 + sign(u) (1/2 - r)
+        const float2 h = add2(both(0.5f), make_float2(-r.x, -r.y));
+        slope = add2(both(0.5f), make_float2(with_sign_of(h.x, u.x), with_sign_of(h.y, u.y)));
+        y = fma2(minus, q, make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
     }
 }
 
 // Whole vectors of eight: a warp takes 512 consecutive elements at a time, two
 // vectors a lane (the layout of block_max), with the next ones' loads in flight.
 template <typename T>
-__global__ void __launch_bounds__(256, 3) taco_gelu_kernel(GeluArgs a)
+__global__ void __launch_bounds__(256, 4) taco_gelu_kernel(GeluArgs a)
 {
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -261,8 +284,32 @@ cudaError_t gelu(const GeluArgs &a, int sms, cudaStream_t stream)
         const int64_t want = (n + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
         return launch_kernel(reinterpret_cast<void *>(&taco_gelu_any_kernel<T>), static_cast<int>(std::min(want, cap)), 256, 0, stream, p);
     }
-    const int64_t want = (n + 4095) / 4096, cap = static_cast<int64_t>(sms) * 3;
+    const int64_t want = (n + 4095) / 4096, cap = static_cast<int64_t>(sms) * 4;
     return launch_kernel(reinterpret_cast<void *>(&taco_gelu_kernel<T>), static_cast<int>(std::min(want, cap)), 256, 0, stream, p);
+}
+
+// Row chunks for a grid of `strips` columns of CTAs: the fewest (up to eight
+// waves of the `slots` CTAs that fit the GPU) that leave at most 3% of the slots
+// without work, or the best there is.  With 64 strips on 304 slots, 4 chunks
+// leave 48 slots idle and 19 fill four waves: 8192 x 16384 takes 164 us
+// against 175.
+int row_chunks(int64_t strips, int64_t passes, int64_t slots)
+{
+    const int64_t most = std::min<int64_t>({passes, kMaxColumnParts, std::max<int64_t>(1, 8 * slots / strips)});
+    int64_t best = 1;
+    double best_share = 0.;
+    for (int64_t n = 1; n <= most; n++) {
+        const int64_t waves = (strips * n + slots - 1) / slots;
+        // the slots' share of work, in whole passes of the longest chunk
+        const double share = static_cast<double>(strips * passes) / static_cast<double>(waves * slots * ((passes + n - 1) / n));
+        if (share > best_share + 1e-9) {
+            best = n;
+            best_share = share;
+        }
+        if (share >= 0.97)
+            break;
+    }
+    return static_cast<int>(best);
 }
 
 template <typename T>
@@ -271,7 +318,7 @@ cudaError_t gelu_grad(GeluGradArgs *a, int sms, cudaStream_t stream)
     const int64_t vectors = a->hidden / 8, strips = (vectors + 31) / 32;
     int strip = static_cast<int>((vectors + strips - 1) / strips);
     const int64_t rows_a_pass = kGradThreads / strip, passes = (a->rows + rows_a_pass - 1) / rows_a_pass;
-    a->nparts = static_cast<int>(std::min<int64_t>({passes, std::max<int64_t>(1, 2 * sms / strips), kMaxColumnParts}));
+    a->nparts = row_chunks(strips, passes, 2 * sms);
     void *p[] = {a, &strip};
     return launch_kernel_2d(reinterpret_cast<void *>(&taco_gelu_grad_kernel<T>), static_cast<unsigned>(strips),
                             static_cast<unsigned>(a->nparts), kGradThreads, 0, stream, p);

@@ -206,17 +206,13 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // *inv receives 1 / s (0 for a zero or non-finite block: all codes are zero).
 __device__ __forceinline__ float record_scale(uint32_t max_bits, int code, float *inv)
 {
-    // Q_max = mantissa * 2^shift with mantissa in [1, 2): 1.75 * 2^8, 1.75 * 2^15, 1.984375 * 2^6.
-    const int shift = code == 0 ? 8 : code == 1 ? 15 : 6;
-    const uint32_t mant = code == 2 ? 0x7e0000u : 0x600000u;
-    if (max_bits == 0u || max_bits >= 0x7f800000u) {
-        *inv = 0.f;
-        return max_bits == 0u ? 0.f : __uint_as_float(0x7fc00000u);
-    }
-    int e = static_cast<int>(max_bits >> 23) - 127 - shift + ((max_bits & 0x7fffffu) > mant ? 1 : 0);
-    e = max(e, -126);
-    *inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    // Q_max = mantissa * 2^shift: 1.75 * 2^8, 1.75 * 2^15, 1.984375 * 2^6.  Adding what a mantissa may lack of 2
+    // carries into the exponent just where c's mantissa exceeds Q_max's.
+    const uint32_t shift = code == 0 ? 8u : code == 1 ? 15u : 6u, room = code == 2 ? 0x1ffffu : 0x1fffffu;
+    const int bits = max(static_cast<int>(((max_bits + room) & 0x7f800000u) - (shift << 23)), 0x00800000);
+    const bool ordinary = max_bits - 1u < 0x7f7fffffu;
+    *inv = ordinary ? __int_as_float(0x7f000000 - bits) : 0.f;
+    return ordinary ? __int_as_float(bits) : max_bits == 0u ? 0.f : __uint_as_float(0x7fc00000u);
 }
 
 // Code byte of u / s (|u / s| <= Q_max; the product with the power of two 1/s is exact
@@ -274,10 +270,11 @@ __device__ __forceinline__ float meta_factor(uint2 m)
 // the two vectors of a pair, whose maxima the caller joins.
 __device__ __forceinline__ uint32_t block_max(const F8 &u, int block)
 {
-    uint32_t top = 0;
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; i++)
-        top = max(top, max(abs_bits(u.v[i].x), abs_bits(u.v[i].y)));
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(u.v[i].x)), "f"(fabsf(u.v[i].y)));
+    uint32_t top = abs_bits(m);                            // a NaN's bits are above infinity's
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1)
         if (8 * d < block)
