@@ -15,14 +15,14 @@ Argument marshalling only, like _binding.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import CODES, _check, _check_cuda_tensor, _stream_handle, compressed_bytes, load_library
+from ._binding import CODES, _check, compressed_bytes, load_library
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _i64, _i32, _f32, _ptr = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p
@@ -58,6 +58,22 @@ class _WeightGradArgs(ctypes.Structure):
                 ("dtype", _i32), ("param_dtype", _i32), ("accumulate", _i32), ("block", _i32), ("code", _i32)]
 
 
+_CALLS = {"taco_layernorm": _LayerNormArgs, "taco_layernorm_backward": _LayerNormBackwardArgs, "taco_gelu": _GeluArgs,
+          "taco_gelu_backward": _GeluBackwardArgs, "taco_weight_grad": _WeightGradArgs}
+
+
+def _packer(kind):
+    """struct.Struct of an argument block: packing a short bytes object costs a
+    fraction of filling a ctypes structure, which counts in small calls."""
+    code = {_ptr: "P", _i64: "q", _i32: "i", _f32: "f"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in kind._fields_) + "0q")
+    assert s.size == ctypes.sizeof(kind)
+    return s.pack
+
+
+_pack_layernorm, _pack_layernorm_backward = _packer(_LayerNormArgs), _packer(_LayerNormBackwardArgs)
+_pack_gelu, _pack_gelu_backward, _pack_weight_grad = _packer(_GeluArgs), _packer(_GeluBackwardArgs), _packer(_WeightGradArgs)
+
 _lib = None
 
 
@@ -65,11 +81,9 @@ def _library() -> ctypes.CDLL:
     global _lib
     if _lib is None:
         lib = load_library()
-        for name, args in (("taco_layernorm", _LayerNormArgs), ("taco_layernorm_backward", _LayerNormBackwardArgs),
-                           ("taco_gelu", _GeluArgs), ("taco_gelu_backward", _GeluBackwardArgs),
-                           ("taco_weight_grad", _WeightGradArgs)):
+        for name in _CALLS:
             fn = getattr(lib, name)
-            fn.argtypes, fn.restype = [ctypes.POINTER(args), _ptr], _i32
+            fn.argtypes, fn.restype = [_ptr, _ptr], _i32
         for name in ("taco_layernorm_backward_workspace", "taco_gelu_backward_workspace"):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = [_i64, _i64], _i64
@@ -107,48 +121,72 @@ def _code(code) -> int:
     return CODES[code] if isinstance(code, str) else int(code)
 
 
-def _tensor(t, name: str, like: torch.Tensor, dtype=None, shape=None) -> int:
-    """Checks one tensor argument (None passes) and returns its address."""
+def _first(x, name: str):
+    """Checks the leading tensor of a call: its dtype's number, rows, hidden."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    kind = DTYPES.get(x.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    shape = x.shape
+    if len(shape) == 2:
+        return kind, shape[0], shape[1]
+    if not shape:
+        raise ValueError("tensor must have at least one dimension")
+    return kind, math.prod(shape[:-1]), shape[-1]
+
+
+def _tensor(t, name: str, device: int, dtype, shape) -> int:
+    """Checks one more tensor and returns its address (0 for None)."""
     if t is None:
-        return None
-    _check_cuda_tensor(t, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype, name)
-    if t.dtype not in DTYPES and t.dtype != torch.uint8:
-        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if shape is not None and t.shape != shape:
+        return 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, not on {device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _rows_hidden(x: torch.Tensor):
-    if x.dim() == 0:
-        raise ValueError("tensor must have at least one dimension")
-    return math.prod(x.shape[:-1]), x.shape[-1]
+def _param_type(t, name: str):
+    if t is None:
+        return torch.float32
+    if not isinstance(t, torch.Tensor) or t.dtype not in DTYPES:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 CUDA tensor")
+    return t.dtype
 
 
-def _packed(packed: torch.Tensor, rows: int, hidden: int, block: int, like: torch.Tensor) -> int:
-    address = _tensor(packed, "packed", like, torch.uint8)
-    nbytes = compressed_bytes(rows, hidden, block)
-    if packed.numel() != nbytes:
-        raise ValueError(f"packed must have {nbytes} bytes, has {packed.numel()}")
-    return address
+def _packed(packed, rows: int, hidden: int, block: int, device: int) -> int:
+    return _tensor(packed, "packed", device, torch.uint8, (compressed_bytes(rows, hidden, block),))
 
 
-class _On(contextlib.ExitStack):
-    """The device and the stream that a call runs on; tensors allocated inside
-    belong to that stream, so one that is freed while the call still runs (a
-    workspace) is reused behind it only."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __init__(self, device: torch.device, stream):
-        super().__init__()
-        if device.index != torch.cuda.current_device():
-            self.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.enter_context(torch.cuda.stream(stream))
-        self.handle = _stream_handle(device, stream)
+
+def _run(device: int, stream, call):
+    """Runs call(handle) on the device and the stream.  Tensors allocated in the
+    call belong to that stream, so one that is freed while the kernels still run
+    (a workspace) is reused behind them only."""
+    if stream is None and device == torch.cuda.current_device():
+        return call(_raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream(device).cuda_stream)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _address(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -159,26 +197,29 @@ def layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opti
     bias share one type.  mean and rstd are float32, one per row.  With
     checkpoint, `packed` holds the normalised rows (before weight and bias) as
     8-bit records."""
-    px = _tensor(x, "x", x)
-    rows, hidden = _rows_hidden(x)
-    pr = _tensor(residual, "residual", x, x.dtype, x.shape)
-    param = weight if weight is not None else bias
-    pdtype = param.dtype if param is not None else torch.float32
-    pw = _tensor(weight, "weight", x, pdtype, (hidden,))
-    pb = _tensor(bias, "bias", x, pdtype, (hidden,))
+    kind, rows, hidden = _first(x, "x")
+    device, shape, width = x.get_device(), x.shape, (hidden,)
+    pdtype = _param_type(weight if weight is not None else bias, "weight")
+    pr = _tensor(residual, "residual", device, x.dtype, shape)
+    pw = _tensor(weight, "weight", device, pdtype, width)
+    pb = _tensor(bias, "bias", device, pdtype, width)
     nbytes = compressed_bytes(rows, hidden, block) if checkpoint else 0
-    with _On(x.device, stream) as on:
+
+    def call(handle):
         y = torch.empty_like(x)
         summed = torch.empty_like(x) if residual is not None else None
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
         packed = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if checkpoint else None
-        args = _LayerNormArgs(px, pr, pw, pb, y.data_ptr(), None if summed is None else summed.data_ptr(),
-                              mean.data_ptr(), rstd.data_ptr(), packed.data_ptr() if checkpoint else None, rows, hidden,
-                              eps, DTYPES[x.dtype], DTYPES[pdtype], block, _code(code))
-        rc = _library().taco_layernorm(args, on.handle)
-    _check(rc, "taco_layernorm")
-    return LayerNorm(y, mean, rstd, summed, packed)
+        rc = _library().taco_layernorm(
+            _pack_layernorm(x.data_ptr(), pr, pw, pb, y.data_ptr(), _address(summed), mean.data_ptr(), rstd.data_ptr(),
+                            _address(packed), rows, hidden, eps, kind, DTYPES[pdtype], block, _code(code)), handle)
+        return rc, LayerNorm(y, mean, rstd, summed, packed)
+
+    rc, result = _run(device, stream, call)
+    if rc:
+        _check(rc, "taco_layernorm")
+    return result
 
 
 def layernorm_backward(dy: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -192,28 +233,36 @@ def layernorm_backward(dy: torch.Tensor, rstd: torch.Tensor, weight: Optional[to
     with bias_grad=False."""
     if (x is None) == (packed is None) or (x is None) != (mean is None):
         raise ValueError("give either x with mean, or packed")
-    pdy = _tensor(dy, "dy", dy)
-    rows, hidden = _rows_hidden(dy)
-    prstd = _tensor(rstd, "rstd", dy, torch.float32, dy.shape[:-1])
-    px = _tensor(x, "x", dy, dy.dtype, dy.shape)
-    pmean = _tensor(mean, "mean", dy, torch.float32, dy.shape[:-1])
-    ppacked = None if packed is None else _packed(packed, rows, hidden, block, dy)
-    pw = _tensor(weight, "weight", dy, None, (hidden,))
-    pds = _tensor(dsummed, "dsummed", dy, dy.dtype, dy.shape)
+    kind, rows, hidden = _first(dy, "dy")
+    device, shape, stats = dy.get_device(), dy.shape, dy.shape[:-1]
+    pdtype = _param_type(weight, "weight")
+    prstd = _tensor(rstd, "rstd", device, torch.float32, stats)
+    px = _tensor(x, "x", device, dy.dtype, shape)
+    pmean = _tensor(mean, "mean", device, torch.float32, stats)
+    ppacked = 0 if packed is None else _packed(packed, rows, hidden, block, device)
+    pw = _tensor(weight, "weight", device, pdtype, (hidden,))
+    pds = _tensor(dsummed, "dsummed", device, dy.dtype, shape)
     lib = _library()
-    with _On(dy.device, stream) as on:
+
+    def call(handle):
         dx = torch.empty_like(dy)
-        dweight = torch.empty_like(weight) if weight is not None else None
-        dbias = torch.empty_like(weight) if weight is not None and bias_grad else None
-        nbytes = lib.taco_layernorm_backward_workspace(rows, hidden) if weight is not None else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
-        args = _LayerNormBackwardArgs(
-            pdy, px, pmean, prstd, ppacked, pw, pds, dx.data_ptr(), None if dweight is None else dweight.data_ptr(),
-            None if dbias is None else dbias.data_ptr(), None if ws is None else ws.data_ptr(), nbytes, rows, hidden,
-            DTYPES[dy.dtype], DTYPES[torch.float32 if weight is None else weight.dtype], block, _code(code))
-        rc = lib.taco_layernorm_backward(args, on.handle)
-    _check(rc, "taco_layernorm_backward")
-    return LayerNormGrads(dx, dweight, dbias)
+        dweight = dbias = ws = None
+        nbytes = 0
+        if weight is not None:
+            dweight = torch.empty_like(weight)
+            dbias = torch.empty_like(weight) if bias_grad else None
+            nbytes = lib.taco_layernorm_backward_workspace(rows, hidden)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
+        rc = lib.taco_layernorm_backward(
+            _pack_layernorm_backward(dy.data_ptr(), px, pmean, prstd, ppacked, pw, pds, dx.data_ptr(), _address(dweight),
+                                     _address(dbias), _address(ws), nbytes, rows, hidden, kind, DTYPES[pdtype], block,
+                                     _code(code)), handle)
+        return rc, LayerNormGrads(dx, dweight, dbias)
+
+    rc, result = _run(device, stream, call)
+    if rc:
+        _check(rc, "taco_layernorm_backward")
+    return result
 
 
 def _tanh_form(approximate: str) -> int:
@@ -226,18 +275,23 @@ def gelu(x: torch.Tensor, bias: Optional[torch.Tensor] = None, approximate: str 
          block: int = 128, code="e4m3", stream=None) -> Gelu:
     """GELU of u = x + bias (added in float32), and the 8-bit records of u."""
     tanh_form = _tanh_form(approximate)
-    px = _tensor(x, "x", x)
-    rows, hidden = _rows_hidden(x)
-    pb = _tensor(bias, "bias", x, None, (hidden,))
+    kind, rows, hidden = _first(x, "x")
+    device = x.get_device()
+    pdtype = _param_type(bias, "bias")
+    pb = _tensor(bias, "bias", device, pdtype, (hidden,))
     nbytes = compressed_bytes(rows, hidden, block) if checkpoint else 0
-    with _On(x.device, stream) as on:
+
+    def call(handle):
         y = torch.empty_like(x)
         packed = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if checkpoint else None
-        args = _GeluArgs(px, pb, y.data_ptr(), packed.data_ptr() if checkpoint else None, rows, hidden, DTYPES[x.dtype],
-                         DTYPES[torch.float32 if bias is None else bias.dtype], tanh_form, block, _code(code))
-        rc = _library().taco_gelu(args, on.handle)
-    _check(rc, "taco_gelu")
-    return Gelu(y, packed)
+        rc = _library().taco_gelu(_pack_gelu(x.data_ptr(), pb, y.data_ptr(), _address(packed), rows, hidden, kind, DTYPES[pdtype],
+                                             tanh_form, block, _code(code)), handle)
+        return rc, Gelu(y, packed)
+
+    rc, result = _run(device, stream, call)
+    if rc:
+        _check(rc, "taco_gelu")
+    return result
 
 
 def gelu_backward(dy: torch.Tensor, packed: torch.Tensor, approximate: str = "none",
@@ -249,23 +303,29 @@ def gelu_backward(dy: torch.Tensor, packed: torch.Tensor, approximate: str = "no
     tanh_form = _tanh_form(approximate)
     if bias_dtype is not None and bias_dtype not in DTYPES:
         raise TypeError(f"bias_dtype must be bfloat16, float16 or float32, got {bias_dtype}")
-    pdy = _tensor(dy, "dy", dy)
-    rows, hidden = _rows_hidden(dy)
-    ppacked = _packed(packed, rows, hidden, block, dy)
+    kind, rows, hidden = _first(dy, "dy")
+    device = dy.get_device()
+    ppacked = _packed(packed, rows, hidden, block, device)
     lib = _library()
-    with _On(dy.device, stream) as on:
+
+    def call(handle):
         dx = torch.empty_like(dy)
         y = torch.empty_like(dy) if recompute else None
-        dbias = torch.empty(hidden, dtype=bias_dtype, device=dy.device) if bias_dtype is not None else None
-        nbytes = lib.taco_gelu_backward_workspace(rows, hidden) if bias_dtype is not None else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
-        args = _GeluBackwardArgs(
-            pdy, ppacked, dx.data_ptr(), None if y is None else y.data_ptr(), None if dbias is None else dbias.data_ptr(),
-            None if ws is None else ws.data_ptr(), nbytes, rows, hidden, DTYPES[dy.dtype],
-            DTYPES[torch.float32 if bias_dtype is None else bias_dtype], tanh_form, block, _code(code))
-        rc = lib.taco_gelu_backward(args, on.handle)
-    _check(rc, "taco_gelu_backward")
-    return GeluGrads(dx, dbias, y)
+        dbias = ws = None
+        nbytes = 0
+        if bias_dtype is not None:
+            dbias = torch.empty(hidden, dtype=bias_dtype, device=dy.device)
+            nbytes = lib.taco_gelu_backward_workspace(rows, hidden)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
+        rc = lib.taco_gelu_backward(
+            _pack_gelu_backward(dy.data_ptr(), ppacked, dx.data_ptr(), _address(y), _address(dbias), _address(ws), nbytes, rows,
+                                hidden, kind, DTYPES[bias_dtype or torch.float32], tanh_form, block, _code(code)), handle)
+        return rc, GeluGrads(dx, dbias, y)
+
+    rc, result = _run(device, stream, call)
+    if rc:
+        _check(rc, "taco_gelu_backward")
+    return result
 
 
 def weight_grad(dy: torch.Tensor, packed: torch.Tensor, hidden: int, block: int = 128, code="e4m3",
@@ -278,33 +338,37 @@ def weight_grad(dy: torch.Tensor, packed: torch.Tensor, hidden: int, block: int 
     dy_sum, the float32 sum of dy over rows (the layer's bias gradient).  The
     result has `dtype` (float32 or bfloat16), or goes to `out`, to which
     accumulate=True adds it."""
-    pdy = _tensor(dy, "dy", dy, torch.bfloat16)
-    rows, features = _rows_hidden(dy)
-    ppacked = _packed(packed, rows, hidden, block, dy)
+    kind, rows, features = _first(dy, "dy")
+    if kind != 0:
+        raise TypeError(f"dy must be torch.bfloat16, got {dy.dtype}")
     if (shift is None) != (dy_sum is None):
         raise ValueError("shift and dy_sum belong together")
-    param = scale if scale is not None else shift
-    pdtype = param.dtype if param is not None else torch.float32
-    pscale = _tensor(scale, "scale", dy, pdtype, (hidden,))
-    pshift = _tensor(shift, "shift", dy, pdtype, (hidden,))
-    psum = _tensor(dy_sum, "dy_sum", dy, torch.float32, (features,))
+    device = dy.get_device()
+    ppacked = _packed(packed, rows, hidden, block, device)
+    pdtype = _param_type(scale if scale is not None else shift, "scale")
+    pscale = _tensor(scale, "scale", device, pdtype, (hidden,))
+    pshift = _tensor(shift, "shift", device, pdtype, (hidden,))
+    psum = _tensor(dy_sum, "dy_sum", device, torch.float32, (features,))
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
     else:
         dtype = out.dtype
-        _tensor(out, "out", dy, dtype, (features, hidden))
-    if dtype not in (torch.float32, torch.bfloat16):
+        _tensor(out, "out", device, dtype, (features, hidden))
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise TypeError(f"the gradient must be float32 or bfloat16, got {dtype}")
     lib = _library()
-    with _On(dy.device, stream) as on:
-        if out is None:
-            out = torch.empty((features, hidden), dtype=dtype, device=dy.device)
-        nbytes = lib.taco_weight_grad_workspace(rows, features, hidden)
+
+    def call(handle):
+        dw = torch.empty((features, hidden), dtype=dtype, device=dy.device) if out is None else out
+        nbytes = max(lib.taco_weight_grad_workspace(rows, features, hidden), 0)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
-        args = _WeightGradArgs(pdy, ppacked, out.data_ptr(), pscale, pshift, psum, None if ws is None else ws.data_ptr(),
-                               max(nbytes, 0), rows, features, hidden, DTYPES[dtype], DTYPES[pdtype], int(accumulate), block,
-                               _code(code))
-        rc = lib.taco_weight_grad(args, on.handle)
-    _check(rc, "taco_weight_grad")
-    return out
+        rc = lib.taco_weight_grad(
+            _pack_weight_grad(dy.data_ptr(), ppacked, dw.data_ptr(), pscale, pshift, psum, _address(ws), nbytes, rows, features,
+                              hidden, DTYPES[dtype], DTYPES[pdtype], int(accumulate), block, _code(code)), handle)
+        return rc, dw
+
+    rc, result = _run(device, stream, call)
+    if rc:
+        _check(rc, "taco_weight_grad")
+    return result
