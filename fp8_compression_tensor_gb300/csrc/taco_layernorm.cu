@@ -95,6 +95,15 @@ __device__ __forceinline__ void group_barrier(int id, int threads)
     asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Sum over the 16 lanes of a half warp.
+__device__ __forceinline__ float half_warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+        v += __shfl_xor_sync(kFullMask, v, d);
+    return v;
+}
+
 // 1 / sqrt(v): the hardware's estimate and one Newton step.
 __device__ __forceinline__ float inv_sqrt(float v)
 {
@@ -276,16 +285,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) taco_norm_kernel(NormArgs a, 
             // at most 16 warps: the two halves of the warp add the same 16 values
             const int w = lane & 15;
             const float2 v = w < warps ? mine_sums[w] : make_float2(0.f, 0.f);
-            sum = v.x;
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1)
-                sum += __shfl_xor_sync(kFullMask, sum, d);
-            mean = sum / fc;
+            mean = half_warp_sum(v.x) / fc;
             const float d = v.x * lane_inv - mean;
-            sq = fmaf(static_cast<float>(lane_n) * d, d, v.y);
-#pragma unroll
-            for (int d2 = 8; d2 > 0; d2 >>= 1)
-                sq += __shfl_xor_sync(kFullMask, sq, d2);
+            sq = half_warp_sum(fmaf(static_cast<float>(lane_n) * d, d, v.y));
         } else {
             mean = sum / fc;
             const float d = pivot - mean;
@@ -551,33 +553,281 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
     }
     if (!a.parts)
         return;
-    // The groups' sums, added in order in the copies' place: for each column eighth four pairs of dweight, four of dbias.
-    float2 *acc = reinterpret_cast<float2 *>(ring);
+    // The groups' sums go to the copies' place, [group][dweight, dbias][C] with the layout of load_plane8, and are added in
+    // the order of the groups.
+    float *acc = reinterpret_cast<float *>(ring) + (groups > 1 ? group * 2 * C : 0);
     copies_landed(0);
-    for (int g = 0; g < groups; g++) {
-        __syncthreads();
-        if (g == group) {
+    __syncthreads();
 #pragma unroll
-            for (int j = 0; j < NV; j++)
-                if (FULL || col[j] < C) {
+    for (int j = 0; j < NV; j++)
+        if (FULL || col[j] < C) {
+            if (groups > 1) {
+                const Raw8<float> w = pack<float>(dw[j]), b = pack<float>(db[j]);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        float2 *w = acc + i * (C / 8) + col[j] / 8, *b = w + C / 2;
-                        if (g > 0) {
-                            dw[j].v[i] = add2(dw[j].v[i], *w);
-                            db[j].v[i] = add2(db[j].v[i], *b);
-                        }
-                        if (g + 1 < groups) {
-                            *w = dw[j].v[i];
-                            *b = db[j].v[i];
-                        }
-                    }
-                    if (g + 1 == groups) {
-                        store_raw8(a.parts + static_cast<int64_t>(blockIdx.x) * C + col[j], pack<float>(dw[j]));
-                        store_raw8(a.parts + static_cast<int64_t>(a.nparts + blockIdx.x) * C + col[j], pack<float>(db[j]));
-                    }
+                for (int k = 0; k < 2; k++) {
+                    *reinterpret_cast<uint4 *>(acc + k * (C / 2) + col[j] / 2) = w.v[k];
+                    *reinterpret_cast<uint4 *>(acc + C + k * (C / 2) + col[j] / 2) = b.v[k];
                 }
+            } else {
+                store_raw8(a.parts + static_cast<int64_t>(blockIdx.x) * C + col[j], pack<float>(dw[j]));
+                store_raw8(a.parts + static_cast<int64_t>(a.nparts + blockIdx.x) * C + col[j], pack<float>(db[j]));
+            }
         }
+    if (groups == 1)
+        return;
+    __syncthreads();
+    acc = reinterpret_cast<float *>(ring);
+    for (int c = threadIdx.x * 4; c < 2 * C; c += blockDim.x * 4) {
+        float4 sum = *reinterpret_cast<const float4 *>(acc + c);
+        for (int g = 1; g < groups; g++) {
+            const float4 v = *reinterpret_cast<const float4 *>(acc + g * 2 * C + c);
+            sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+        }
+        // place c of the planes: half k of the eight columns from `eight` on
+        const int which = c >= C, at = c - which * C, k = at >= C / 2, eight = (at - k * (C / 2)) * 2;
+        *reinterpret_cast<float4 *>(a.parts + static_cast<int64_t>(which * a.nparts + blockIdx.x) * C + eight + 4 * k) = sum;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Widths that are no multiple of 8 (rows that start at any element)
+// ---------------------------------------------------------------------------
+
+// The layout of the kernels above, with a lane's eight elements 32 apart, so a
+// warp reads and writes consecutive elements.  The group copies its rows to
+// shared memory in 16-byte pieces from the boundary below the row's first
+// element, and reads them behind a barrier, on the schedule of record bytes
+// above.  A row's place holds whole vectors; what lies past the row is ignored.
+
+template <typename T>
+__device__ __forceinline__ void copy_odd_row(uint32_t to, const void *base, int64_t row, int64_t rows, int C, int thread, int threads)
+{
+    const int64_t first = row * C * static_cast<int>(sizeof(T)), at = first & ~int64_t{15}, left = rows * C * static_cast<int>(sizeof(T)) - at;
+    const int bytes = static_cast<int>(first - at) + C * static_cast<int>(sizeof(T));
+    for (int c = thread * 16; c < bytes; c += threads * 16)
+        copy16_part(to + c, static_cast<const uint8_t *>(base) + at + c, left - c < 16 ? static_cast<int>(left - c) : 16);
+}
+
+// Where the row's element 0 lies in its place.
+template <typename T>
+__device__ __forceinline__ int odd_shift(int64_t row, int C)
+{
+    return static_cast<int>(row * C * static_cast<int>(sizeof(T)) & 15);
+}
+
+__host__ __device__ constexpr int odd_room(int width, int element) { return width * element + 32; }
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kNormThreads, 1) taco_norm_odd_kernel(NormArgs a, int warps, int groups, int stages)
+{
+    extern __shared__ __align__(16) uint8_t dynamic[];   // weight, bias, then the copies
+    __shared__ float2 sums[2][32];
+    grid_launch_dependents();
+    constexpr int N = 8 * NV;
+    const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
+    const int C = static_cast<int>(a.hidden), c0 = warp * 32 * N + lane;
+    const float fc = static_cast<float>(C);
+    const int warp_n = min(max(C - warp * 32 * N, 0), 32 * N), lane_n = min(max(C - (lane & 15) * 32 * N, 0), 32 * N);
+    const float warp_inv = warp_n > 0 ? 1.f / static_cast<float>(warp_n) : 0.f;
+    const float lane_inv = lane_n > 0 ? 1.f / static_cast<float>(lane_n) : 0.f;
+    const int room = odd_room(warps * 32 * N, sizeof(T)), tensors = a.residual ? 2 : 1, stage_bytes = groups * tensors * room;
+    float *sparam = reinterpret_cast<float *>(dynamic);
+    uint8_t *ring = dynamic + (8 * C + 15) / 16 * 16 + group * tensors * room;
+    grid_dependency_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group, step = static_cast<int64_t>(gridDim.x) * groups;
+    auto copy_row = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            const uint32_t to = smem_addr(ring) + static_cast<uint32_t>(stage * stage_bytes);
+            copy_odd_row<T>(to, a.x, row, a.rows, C, warp * 32 + lane, warps * 32);
+            if (a.residual)
+                copy_odd_row<T>(to + room, a.residual, row, a.rows, C, warp * 32 + lane, warps * 32);
+        }
+        copies_issued();
+    };
+    for (int i = 0; i < stages - 1; i++)
+        copy_row(first + i * step, i);
+    for (int c = threadIdx.x; c < C; c += blockDim.x) {
+        sparam[c] = a.weight ? load_param(a.weight, a.param_dtype, c) : 1.f;
+        sparam[C + c] = a.bias ? load_param(a.bias, a.param_dtype, c) : 0.f;
+    }
+    copies_landed(stages - 2);
+    __syncthreads();
+    int stage = 0, fill = stages - 1;
+    uint32_t side = 0;
+    for (int64_t row = first; row < a.rows; row += step, side ^= 1u) {
+        const T *x = reinterpret_cast<const T *>(ring + stage * stage_bytes + odd_shift<T>(row, C)) + c0;
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        float h[N], sum = 0.f, sq = 0.f, mean;
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            h[i] = to_float(x[32 * i]);
+        if (a.residual) {
+            const T *res = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(x) + room);
+            T *out = static_cast<T *>(a.summed) + row * C + c0;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const T v = from_float<T>(h[i] + to_float(res[32 * i]));
+                if (c0 + 32 * i < C)
+                    out[32 * i] = v;
+                h[i] = to_float(v);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            h[i] = c0 + 32 * i < C ? h[i] : 0.f;
+            sum += h[i];
+        }
+        sum = warp_sum(sum);
+        const float pivot = sum * warp_inv;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float d = c0 + 32 * i < C ? h[i] - pivot : 0.f;
+            sq = fmaf(d, d, sq);
+        }
+        sq = warp_sum(sq);
+        copies_landed(stages - 3);
+        if (warps > 1) {
+            float2 *mine_sums = sums[side] + group * warps;
+            if (lane == 0)
+                mine_sums[warp] = make_float2(sum, sq);
+            group_barrier(1 + group, warps * 32);
+            const int w = lane & 15;
+            const float2 v = w < warps ? mine_sums[w] : make_float2(0.f, 0.f);
+            mean = half_warp_sum(v.x) / fc;
+            const float d = v.x * lane_inv - mean;
+            sq = half_warp_sum(fmaf(static_cast<float>(lane_n) * d, d, v.y));
+        } else {
+            __syncwarp();
+            mean = sum / fc;
+            sq = fmaf(fc * (pivot - mean), pivot - mean, sq);
+        }
+        copy_row(row + (stages - 1) * step, fill);
+        fill = fill + 1 == stages ? 0 : fill + 1;
+        const float rstd = inv_sqrt(sq / fc + a.eps);
+        if (warp == 0 && lane == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        T *y = static_cast<T *>(a.y) + row * C + c0;
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (c0 + 32 * i < C)
+                y[32 * i] = from_float<T>(fmaf((h[i] - mean) * rstd, sparam[c0 + 32 * i], sparam[C + c0 + 32 * i]));
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kGradThreads, 1) taco_norm_grad_odd_kernel(NormGradArgs a, int warps, int groups, int stages)
+{
+    extern __shared__ __align__(16) uint8_t dynamic[];   // weight, then the copies; then the groups' column sums
+    __shared__ float2 sums[2][32];
+    grid_launch_dependents();
+    constexpr int N = 8 * NV;
+    const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
+    const int C = static_cast<int>(a.hidden), c0 = warp * 32 * N + lane;
+    const float inv_c = 1.f / static_cast<float>(C);
+    const int room = odd_room(warps * 32 * N, sizeof(T)), tensors = a.dsummed ? 3 : 2, stage_bytes = groups * tensors * room;
+    float *sweight = reinterpret_cast<float *>(dynamic);                 // whole vectors, zeros past the row
+    uint8_t *ring = dynamic + warps * 32 * N * 4 + group * tensors * room;
+    grid_dependency_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group, step = static_cast<int64_t>(gridDim.x) * groups;
+    auto copy_row = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            const uint32_t to = smem_addr(ring) + static_cast<uint32_t>(stage * stage_bytes);
+            copy_odd_row<T>(to, a.dy, row, a.rows, C, warp * 32 + lane, warps * 32);
+            copy_odd_row<T>(to + room, a.x, row, a.rows, C, warp * 32 + lane, warps * 32);
+            if (a.dsummed)
+                copy_odd_row<T>(to + 2 * room, a.dsummed, row, a.rows, C, warp * 32 + lane, warps * 32);
+        }
+        copies_issued();
+    };
+    float next_rstd = 0.f, next_mean = 0.f;
+    auto fetch = [&](int64_t row) {
+        if (row < a.rows) {
+            next_rstd = __ldg(a.rstd + row);
+            next_mean = __ldg(a.mean + row);
+        }
+    };
+    for (int i = 0; i < stages - 1; i++)
+        copy_row(first + i * step, i);
+    fetch(first);
+    for (int c = threadIdx.x; c < warps * 32 * N; c += blockDim.x)
+        sweight[c] = c >= C ? 0.f : a.weight ? load_param(a.weight, a.param_dtype, c) : 1.f;
+    copies_landed(stages - 2);
+    __syncthreads();
+    const float *weight = sweight + c0;
+    float dw[N], db[N];
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        dw[i] = db[i] = 0.f;
+    int stage = 0, fill = stages - 1;
+    uint32_t side = 0;
+    for (int64_t row = first; row < a.rows; row += step, side ^= 1u) {
+        const uint8_t *place = ring + stage * stage_bytes + odd_shift<T>(row, C);
+        const T *dy = reinterpret_cast<const T *>(place) + c0, *x = reinterpret_cast<const T *>(place + room) + c0,
+                *ds = reinterpret_cast<const T *>(place + 2 * room) + c0;
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        const float rstd = next_rstd, mean = next_mean;
+        fetch(row + step);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float w = to_float(dy[32 * i]) * weight[32 * i], xh = (to_float(x[32 * i]) - mean) * rstd;
+            s1 += c0 + 32 * i < C ? w : 0.f;
+            s2 += c0 + 32 * i < C ? w * xh : 0.f;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            s1 += __shfl_xor_sync(kFullMask, s1, d);
+            s2 += __shfl_xor_sync(kFullMask, s2, d);
+        }
+        copies_landed(stages - 3);
+        if (warps > 1) {
+            float2 *mine_sums = sums[side] + group * warps;
+            if (lane == 0)
+                mine_sums[warp] = make_float2(s1, s2);
+            group_barrier(1 + group, warps * 32);
+            const float2 v = (lane & 15) < warps ? mine_sums[lane & 15] : make_float2(0.f, 0.f);
+            s1 = half_warp_sum(v.x);
+            s2 = half_warp_sum(v.y);
+        } else {
+            __syncwarp();
+        }
+        copy_row(row + (stages - 1) * step, fill);
+        fill = fill + 1 == stages ? 0 : fill + 1;
+        const float c1 = s1 * inv_c, c2 = s2 * inv_c;
+        T *dx = static_cast<T *>(a.dx) + row * C + c0;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float g = to_float(dy[32 * i]), xh = (to_float(x[32 * i]) - mean) * rstd;
+            dw[i] = fmaf(g, xh, dw[i]);               // what lies past the row is never written out
+            db[i] += g;
+            float v = rstd * fmaf(-xh, c2, fmaf(g, weight[32 * i], -c1));
+            if (a.dsummed)
+                v += to_float(ds[32 * i]);
+            if (c0 + 32 * i < C)
+                dx[32 * i] = from_float<T>(v);
+        }
+    }
+    if (!a.parts)
+        return;
+    // The groups' sums, [group][dweight, dbias][C], added in the order of the groups.
+    float *shared = reinterpret_cast<float *>(dynamic);
+    copies_landed(0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        if (c0 + 32 * i < C) {
+            shared[group * 2 * C + c0 + 32 * i] = dw[i];
+            shared[group * 2 * C + C + c0 + 32 * i] = db[i];
+        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * C; c += blockDim.x) {
+        float sum = shared[c];
+        for (int g = 1; g < groups; g++)
+            sum += shared[g * 2 * C + c];
+        const int which = c >= C;
+        a.parts[static_cast<int64_t>(which * a.nparts + blockIdx.x) * C + c - which * C] = sum;
     }
 }
 
@@ -641,7 +891,7 @@ int row_grid(int64_t rows, int sms, int per_sm)
 constexpr int kMaxVectorWidth = 16 * 4 * 256;
 constexpr size_t kMaxShared = 225 * 1024;
 
-bool fits_registers(int64_t hidden) { return hidden % 8 == 0 && hidden <= kMaxVectorWidth; }
+bool fits_registers(int64_t hidden) { return hidden <= kMaxVectorWidth; }
 
 // Vectors a lane: four, or what a single warp needs for a short row.
 int lane_vectors(int64_t hidden) { return hidden <= 256 ? 1 : hidden <= 512 ? 2 : 4; }
@@ -669,12 +919,72 @@ const void *norm_kernel(int nv, bool staged, bool full)
     return staged ? norm_kernel<T, true>(nv, full) : norm_kernel<T, false>(nv, full);
 }
 
+template <typename T>
+const void *norm_odd_kernel(int nv)
+{
+    return nv == 1   ? reinterpret_cast<void *>(&taco_norm_odd_kernel<T, 1>)
+           : nv == 2 ? reinterpret_cast<void *>(&taco_norm_odd_kernel<T, 2>)
+                     : reinterpret_cast<void *>(&taco_norm_odd_kernel<T, 4>);
+}
+
+template <typename T>
+const void *norm_grad_odd_kernel(int nv)
+{
+    return nv == 1   ? reinterpret_cast<void *>(&taco_norm_grad_odd_kernel<T, 1>)
+           : nv == 2 ? reinterpret_cast<void *>(&taco_norm_grad_odd_kernel<T, 2>)
+                     : reinterpret_cast<void *>(&taco_norm_grad_odd_kernel<T, 4>);
+}
+
 // Rows in flight: up to four in the shared memory that the parameters leave.
 int ring_stages(size_t params, size_t stage, int most = 4)
 {
     while (most > 1 && params + most * stage > kMaxShared)
         most--;
     return most;
+}
+
+// Kernel and shape for odd widths; false where three rows do not fit shared memory.
+template <typename T>
+bool norm_odd(const NormArgs &a, int sms, cudaStream_t stream, cudaError_t *result)
+{
+    NormArgs args = a;
+    const int nv = lane_vectors(a.hidden);
+    int warps = static_cast<int>((a.hidden + 256 * nv - 1) / (256 * nv));
+    int groups = row_groups(a.rows, warps, kNormThreads, sms);
+    const size_t params = (8 * static_cast<size_t>(a.hidden) + 15) / 16 * 16;
+    const size_t place = static_cast<size_t>(a.residual ? 2 : 1) * odd_room(warps * nv * 256, sizeof(T));
+    while (groups > 1 && ring_stages(params, groups * place) < 3)
+        groups--;
+    const size_t stage = groups * place;
+    int stages = ring_stages(params, stage);
+    if (stages < 3)
+        return false;
+    void *p[] = {&args, &warps, &groups, &stages};
+    *result = launch_kernel(norm_odd_kernel<T>(nv), static_cast<int>(std::min<int64_t>((a.rows + groups - 1) / groups, sms)),
+                            warps * groups * 32, params + stages * stage, stream, p);
+    return true;
+}
+
+template <typename T>
+bool norm_grad_odd(NormGradArgs *a, int sms, cudaStream_t stream, cudaError_t *result)
+{
+    const int nv = lane_vectors(a->hidden);
+    int warps = static_cast<int>((a->hidden + 256 * nv - 1) / (256 * nv));
+    int groups = row_groups(a->rows, warps, kGradThreads, sms);
+    const size_t weight = static_cast<size_t>(warps) * nv * 1024;
+    const size_t place = static_cast<size_t>(a->dsummed ? 3 : 2) * odd_room(warps * nv * 256, sizeof(T));
+    while (groups > 1 && ring_stages(weight, groups * place) < 3)
+        groups--;
+    const size_t stage = groups * place;
+    int stages = ring_stages(weight, stage);
+    if (stages < 3)
+        return false;
+    a->nparts = static_cast<int>(std::min({(a->rows + groups - 1) / groups, static_cast<int64_t>(sms),
+                                           static_cast<int64_t>(kMaxColumnParts)}));
+    void *p[] = {a, &warps, &groups, &stages};
+    *result = launch_kernel(norm_grad_odd_kernel<T>(nv), a->nparts, warps * groups * 32,
+                            std::max(weight + stages * stage, 8 * static_cast<size_t>(a->hidden) * groups), stream, p);
+    return true;
 }
 
 template <typename T>
@@ -698,8 +1008,11 @@ cudaError_t norm_vectors(const NormArgs &a, int sms, cudaStream_t stream)
 template <typename T>
 cudaError_t norm_any(const NormArgs &a, int sms, cudaStream_t stream)
 {
-    if (fits_registers(a.hidden))
+    cudaError_t result;
+    if (fits_registers(a.hidden) && a.hidden % 8 == 0)
         return norm_vectors<T>(a, sms, stream);
+    if (fits_registers(a.hidden) && norm_odd<T>(a, sms, stream, &result))
+        return result;
     NormArgs args = a;
     void *p[] = {&args};
     return launch_kernel(reinterpret_cast<void *>(&taco_norm_any_kernel<T>), row_grid(a.rows, sms, 8), kRowThreads, 0,
@@ -725,7 +1038,10 @@ template <typename T>
 cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
 {
     const int64_t C = a->hidden;
-    if (fits_registers(C)) {
+    cudaError_t result;
+    if (fits_registers(C) && C % 8 && norm_grad_odd<T>(a, sms, stream, &result))
+        return result;
+    if (fits_registers(C) && C % 8 == 0) {
         const bool records = !a->x;
         const int nv = lane_vectors(C);
         int warps = static_cast<int>((C + 256 * nv - 1) / (256 * nv));
@@ -736,7 +1052,7 @@ cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
         if (records)
             stage += static_cast<size_t>(groups) * ((C / a->block * (a->block + 8) + 8 + 15) / 16 * 16);
         int stages = ring_stages(weight, stage);
-        const size_t smem = weight + std::max<size_t>(stages * stage, groups > 1 ? 8 * static_cast<size_t>(C) : 0);
+        const size_t smem = weight + std::max<size_t>(stages * stage, groups > 1 ? 8 * static_cast<size_t>(C) * groups : 0);
         if (smem <= kMaxShared && (!records || stages >= 3)) {
             a->nparts = static_cast<int>(std::min({(a->rows + groups - 1) / groups, static_cast<int64_t>(sms),
                                                    static_cast<int64_t>(kMaxColumnParts)}));
@@ -757,9 +1073,13 @@ template <typename T>
 cudaError_t init_norm_type()
 {
     for (int nv = 1; nv <= 4; nv *= 2)
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < 10; i++) {
             const bool flag = i & 1, full = i & 2;
-            const cudaError_t e = cudaFuncSetAttribute(i < 4 ? norm_kernel<T>(nv, flag, full) : norm_grad_kernel<T>(nv, flag, full),
+            const void *kernel = i < 4   ? norm_kernel<T>(nv, flag, full)
+                                 : i < 8 ? norm_grad_kernel<T>(nv, flag, full)
+                                 : i < 9 ? norm_odd_kernel<T>(nv)
+                                         : norm_grad_odd_kernel<T>(nv);
+            const cudaError_t e = cudaFuncSetAttribute(kernel,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxShared));
             if (e != cudaSuccess)
                 return e;
