@@ -85,6 +85,8 @@ void init_device(DeviceState &st)
         e = init_weight_grad();
     if (e == cudaSuccess)
         e = init_norm();
+    if (e == cudaSuccess)
+        e = init_norm_grad();
     st.init_error = e;
 }
 

@@ -67,6 +67,7 @@ struct WeightGradArgs {
 // Kernel attributes, once per device.
 cudaError_t init_weight_grad();
 cudaError_t init_norm();
+cudaError_t init_norm_grad();
 
 cudaError_t launch_norm(int dtype, const NormArgs &a, int sms, cudaStream_t stream);
 // The gradient launches set nparts to the number of row chunks they use (at most what the caller gives).
