@@ -227,12 +227,13 @@ __global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGra
     for (int i = 0; i < 4; i++)
         db.v[i] = both(0.f);
     Raw8<T> next_dy;
-    uint2 next_codes = {}, next_meta = {};
+    uint2 next_codes = {};
+    float next_s = 0.f;
     auto fetch = [&](int64_t row) {
         if (in && row < a.rows) {
             next_dy = load_raw8(static_cast<const T *>(a.dy) + row * C + col);
             next_codes = __ldg(reinterpret_cast<const uint2 *>(rec + row * pitch + within));
-            next_meta = __ldg(reinterpret_cast<const uint2 *>(rec + row * pitch + a.block));
+            next_s = __ldg(reinterpret_cast<const float *>(rec + row * pitch + a.block + 4));
         }
     };
     int64_t row = static_cast<int64_t>(blockIdx.y) * rows_a_pass + mine;
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGra
     if (in)
         for (; row < a.rows; row += step) {
             const F8 g = unpack(next_dy), q = codes8_to_float(next_codes, a.code);
-            const float s = meta_factor(next_meta);
+            const float s = next_s;
             fetch(row + step);
             F8 d, y;
 #pragma unroll

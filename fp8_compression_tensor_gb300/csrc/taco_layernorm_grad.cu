@@ -186,7 +186,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
 #pragma unroll
             for (int j = 0; j < NV; j++)
                 if (FULL || col[j] < C)
-                    factor[j] = meta_factor(*reinterpret_cast<const uint2 *>(rec + (col[j] >> shift) * (a.block + 8) + a.block));
+                    factor[j] = record_s(rec + (col[j] >> shift) * (a.block + 8), a.block);
         }
         auto normalised = [&](int j) {
             if (RECORDS)
@@ -251,6 +251,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
             if (FULL || col[j] < C) {
                 const F8 g = vector(0, j), q = normalised(j);
                 const float f = RECORDS ? factor[j] : 1.f;
+                asm volatile("" ::: "memory");   // the weights are read again rather than kept over the row sums
                 F8 w = weighted(j, g);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {

@@ -257,11 +257,10 @@ __device__ __forceinline__ F8 codes8_to_float(uint2 c, int code)
     return f;
 }
 
-// Factor s / alpha of a record's (alpha, s).
-__device__ __forceinline__ float meta_factor(uint2 m)
+// A record's s.  Checkpoints are DS-only records, whose alpha is 1: it is not read.
+__device__ __forceinline__ float record_s(const uint8_t *rec, int block)
 {
-    const float alpha = __uint_as_float(m.x), s = __uint_as_float(m.y);
-    return alpha == 1.f ? s : __fdiv_rn(s, alpha);
+    return *reinterpret_cast<const float *>(rec + block + 4);
 }
 
 // The scale of the block that this lane's eight values belong to and their
@@ -324,20 +323,12 @@ __device__ __forceinline__ int64_t record_offset(int64_t col, int block)
     return k * (block + 8) + (col - k * block);
 }
 
-// s / alpha of a record (alpha is 1 in the records written here).
-__device__ __forceinline__ float record_factor(const uint8_t *rec, int block)
-{
-    const uint2 m = *reinterpret_cast<const uint2 *>(rec + block);
-    const float alpha = __uint_as_float(m.x), s = __uint_as_float(m.y);
-    return alpha == 1.f ? s : __fdiv_rn(s, alpha);
-}
-
 // Value of element (row, col) of packed records of [rows, hidden].
 __device__ __forceinline__ float record_value(const uint8_t *packed, int64_t index, int block, int code)
 {
     const int64_t k = index / block;
     const uint8_t *rec = packed + k * (block + 8);
-    return codes2_to_float2(rec[index - k * block], code).x * record_factor(rec, block);
+    return codes2_to_float2(rec[index - k * block], code).x * record_s(rec, block);
 }
 
 // ---------------------------------------------------------------------------

@@ -250,6 +250,13 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
         : "memory");
 }
 
+__device__ __forceinline__ float lds_float(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
 // 16 consecutive tensor-memory columns of this thread's lane, complete on return.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -526,33 +533,21 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             plan.at(u, m0, n0, split, first, count);
             const RawSpan at(n0 + static_cast<int64_t>(rank) * 128, a.block, odd_shift);
             const uint32_t code_at = row_at + at.shift[sub] + col / span * (span + 8) + col % span;
-            const uint32_t meta_at = a.block > 128 ? meta_row_at + at.meta_shift[sub]
-                                                   : row_at + at.shift[sub] + col / span * (span + 8) + span;
-            const uint32_t meta_pitch = a.block > 128 ? 16u : static_cast<uint32_t>(raw_width);
+            const uint32_t s_at = 4u + (a.block > 128 ? meta_row_at + at.meta_shift[sub]
+                                                   : row_at + at.shift[sub] + col / span * (span + 8) + span);
+            const uint32_t s_pitch = a.block > 128 ? 16u : static_cast<uint32_t>(raw_width);
             for (int k = 0; k < count; k++) {
                 if (!mbar_wait_bounded(bar(bars.raw_full[slot]), raw_phase, fault, kFaultWeightGrad)) {
                     ok = false;
                     break;
                 }
                 const uint32_t src = raw + static_cast<uint32_t>(slot) * kRawBytes;
-                uint2 c[4], meta[4];
-                uint32_t other = 0;                            // nonzero where some alpha is not 1
+                uint2 c[4];
+                float f[4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     c[j] = lds64(src + code_at + j * raw_width);
-                    meta[j] = lds64(src + meta_at + j * meta_pitch);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    other |= meta[j].y ? meta[j].x ^ 0x3f800000u : 0u;   // s = 0: all zero, as past the tensor's end
-                if (__any_sync(kFullMask, other != 0u)) {      // records of compress
-#pragma unroll 1
-                    for (int i = 0; i < 4; i++) {
-#pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            if (i == j && meta[j].y)
-                                meta[j].y = __float_as_uint(__fdiv_rn(__uint_as_float(meta[j].y), __uint_as_float(meta[j].x)));
-                    }
+                    f[j] = lds_float(src + s_at + j * s_pitch);
                 }
                 __syncwarp();                                  // the warp has read the slot
                 if (lane == 0)
@@ -564,7 +559,7 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                 const uint32_t dst = base + s * 2 * kOperandBytes;
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    sts128(dst + place[j], decode8<CODE>(c[j], __uint_as_float(meta[j].y)));
+                    sts128(dst + place[j], decode8<CODE>(c[j], f[j]));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)

@@ -190,7 +190,8 @@ TACO_API taco_status_t taco_reduce_shards_ex(const void *const *packed_shards, i
  * infinity or a NaN gets s = NaN and decodes to NaN.  taco_decompress_ex with
  * TACO_VARIANT_DS_ONLY decodes it; its values q s are exact in bf16 (above
  * bf16's subnormal range).  The backward calls below take any DS-only records,
- * also those of taco_compress_ex, and decode them as q (s / alpha).
+ * also those of taco_compress_ex, and decode them as q s (DS-only records have
+ * alpha = 1; it is not read).
  *
  * The common rules above hold, and:
  *   - Tensors are row-major [rows, hidden] (leading dimensions flattened) of
