@@ -143,22 +143,22 @@ __global__ void __launch_bounds__(256) taco_weight_grad_any_kernel(WeightGradArg
 constexpr int kPairM = 256, kPairN = 256;     // tile of a CTA pair; each CTA holds 128 rows of A and of B
 constexpr int kStageRows = 64;                // rows of dY and X per pipeline stage
 constexpr int kChunkRows = 1024;              // rows per tensor-core accumulation
-constexpr int kStages = 5, kRawStages = 5;
+constexpr int kStages = 5;                    // of both operands and of the record bytes
 constexpr int kOperandBytes = 128 * kStageRows * 2;             // one CTA's A or B of a stage
 constexpr int kHalfBytes = 64 * kStageRows * 2;                 // 64 columns of it
-constexpr int kDecoders = 8;                                     // decoder warps, 8 rows of a stage each
+constexpr int kTeam = 4;                                         // decoder warps of a stage, 16 rows each; two teams
 constexpr int kRawWidth = 176;                                   // widest box of record bytes: 4 records of B = 32, and 8 bytes of slack
 constexpr int kRawBytes = kStageRows * (kRawWidth + 16);         // even rows, odd rows, then their scales where they lie apart
 constexpr int kWgThreads = 640;
-constexpr size_t kWgSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOperandBytes + kRawStages * kRawBytes + 512;
+constexpr size_t kWgSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOperandBytes + kStages * kRawBytes + 512;
 constexpr uint32_t kIdesc = mma_idesc_bf16_f32(kPairM, kPairN) | (1u << 15) | (1u << 16);   // A and B MN-major
 
 struct WgBarriers {
     uint64_t a_full[kStages];     // this CTA's dY tile has landed
     uint64_t full[kStages];       // even CTA: both CTAs' A and B of the stage are ready
     uint64_t empty[kStages];      // the stage's products are done
-    uint64_t raw_full[kRawStages];    // record bytes have landed
-    uint64_t raw_empty[kRawStages];   // and have been decoded
+    uint64_t raw_full[kStages];    // record bytes have landed
+    uint64_t raw_empty[kStages];   // and have been decoded
     uint64_t acc_full[2];         // a chunk's accumulator is complete
     uint64_t acc_empty[2];        // even CTA: both CTAs have read the accumulator
     uint32_t tmem;
@@ -335,7 +335,7 @@ struct RawSpan {
 // parity has a map of its own.  The odd rows' map then starts 8 bytes before the
 // first of them (odd_shift = 8) to be 16-byte aligned.  No map reaches past the
 // buffer; rows and columns past the tensor read zeros.  Copying eight bytes a
-// lane with cp.async instead took 1.79 ms at 8192 x 16384 x 4096, this 0.84 ms.
+// lane with cp.async instead took 1.79 ms at 8192 x 16384 x 4096, this 0.84 ms (then).
 struct RawMaps {
     CUtensorMap even, odd;            // boxes of `width` bytes by 32 rows
     CUtensorMap meta_even, meta_odd;  // boxes of 16 bytes by 32 rows (blocks above 128)
@@ -359,12 +359,12 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(bar(bars.a_full[s]), 1);
-            mbar_init(bar(bars.full[s]), 2 * (kDecoders + 1));   // each CTA's decoders, and its dY tile
+            mbar_init(bar(bars.full[s]), 2 * (kTeam + 1));   // each CTA's decoders, and its dY tile
             mbar_init(bar(bars.empty[s]), 1);
         }
-        for (int s = 0; s < kRawStages; s++) {
+        for (int s = 0; s < kStages; s++) {
             mbar_init(bar(bars.raw_full[s]), 1);
-            mbar_init(bar(bars.raw_empty[s]), kDecoders);
+            mbar_init(bar(bars.raw_empty[s]), kTeam);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(bar(bars.acc_full[b]), 1);
@@ -477,14 +477,14 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                         tma_load_2d(dst + kStageRows * kRawWidth + 512, &raw_maps.meta_odd, at.meta_x[1], y + odd_row0, full);
                     }
                     used |= 1u << s;
-                    if (++s == kRawStages) {
+                    if (++s == kStages) {
                         s = 0;
                         phase ^= 1u;
                     }
                 }
             }
             // no copy may land after the CTA is gone: the last phase of every slot that was filled
-            for (int i = 0; i < kRawStages; i++)
+            for (int i = 0; i < kStages; i++)
                 if (used >> i & 1u)
                     mbar_wait_bounded_thread(bar(bars.raw_full[i]), i < s ? phase : phase ^ 1u, fault, kFaultWeightGrad);
         } else if (warp == 3 && lane == 0) {
@@ -508,25 +508,27 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                 }
             }
         }
-    } else if (warp < 4 + kDecoders) {
+    } else if (warp < 4 + 2 * kTeam) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        // Decoders: warp d takes rows 8 d .. 8 d + 7 of every stage; lane l the
-        // codes 8 (l % 16) .. of rows l / 16, l / 16 + 2, ...
-        const int d = warp - 4, sub = lane >> 4, col = (lane & 15) * 8;
+        // Decoders: two teams of four warps take the stages in turn, so a team's
+        // waits, loads and fence run while the other team converts.  Warp d of a
+        // team takes rows 16 d .. 16 d + 15 of its stage; lane l the codes 8 (l %
+        // 16) .. of rows l / 16, l / 16 + 2, ...
+        const int team = (warp - 4) >> 2, d = warp & 3, sub = lane >> 4, col = (lane & 15) * 8;
         const int span = min(a.block, 128);                    // codes of a row's 128 columns lie in pieces of `span`
         const uint32_t swz = static_cast<uint32_t>(lane & 7);
         const uint32_t full0 = in_even_cta(bar(bars.full[0]));
-        const uint32_t row_at = static_cast<uint32_t>(sub * (kStageRows / 2) * kRawWidth + d * 4 * raw_width);
-        const uint32_t meta_row_at = static_cast<uint32_t>(kStageRows * kRawWidth + sub * 512 + d * 64);
-        // Swizzled place of this lane's 16 bytes: row 8 d + 2 j + sub.
+        const uint32_t row_at = static_cast<uint32_t>(sub * (kStageRows / 2) * kRawWidth + d * 8 * raw_width);
+        const uint32_t meta_row_at = static_cast<uint32_t>(kStageRows * kRawWidth + sub * 512 + d * 128);
+        // Swizzled place of this lane's 16 bytes: row 16 d + 2 j + sub (rows 8 apart share the swizzle).
         uint32_t place[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const uint32_t kr = static_cast<uint32_t>(2 * j + sub);
-            place[j] = static_cast<uint32_t>(kOperandBytes + (col >> 6) * kHalfBytes + d * 1024) + kr * 128 + ((swz ^ kr) << 4);
+            place[j] = static_cast<uint32_t>(kOperandBytes + (col >> 6) * kHalfBytes + d * 2048) + kr * 128 + ((swz ^ kr) << 4);
         }
-        int s = 0, slot = 0;
-        uint32_t phase = 0, raw_phase = 0;
+        int s = 0, turn = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
             int m0, n0, split, first, count;
@@ -536,37 +538,40 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             const uint32_t s_at = 4u + (a.block > 128 ? meta_row_at + at.meta_shift[sub]
                                                    : row_at + at.shift[sub] + col / span * (span + 8) + span);
             const uint32_t s_pitch = a.block > 128 ? 16u : static_cast<uint32_t>(raw_width);
-            for (int k = 0; k < count; k++) {
-                if (!mbar_wait_bounded(bar(bars.raw_full[slot]), raw_phase, fault, kFaultWeightGrad)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t src = raw + static_cast<uint32_t>(slot) * kRawBytes;
-                uint2 c[4];
-                float f[4];
+            for (int k = 0; k < count; k++, turn ^= 1) {
+                if (turn == team) {
+                    if (!mbar_wait_bounded(bar(bars.raw_full[s]), phase, fault, kFaultWeightGrad)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t src = raw + static_cast<uint32_t>(s) * kRawBytes, dst = base + s * 2 * kOperandBytes;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    c[j] = lds64(src + code_at + j * raw_width);
-                    f[j] = lds_float(src + s_at + j * s_pitch);
-                }
-                __syncwarp();                                  // the warp has read the slot
-                if (lane == 0)
-                    mbar_arrive(bar(bars.raw_empty[slot]));
-                if (!mbar_wait_bounded(bar(bars.empty[s]), phase ^ 1u, fault, kFaultWeightGrad)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = base + s * 2 * kOperandBytes;
+                    for (int h = 0; h < 2; h++) {
+                        uint2 c[4];
+                        float f[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    sts128(dst + place[j], decode8<CODE>(c[j], f[j]));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    cluster_arrive(full0 + s * 8);
-                if (++slot == kRawStages) {
-                    slot = 0;
-                    raw_phase ^= 1u;
+                        for (int j = 0; j < 4; j++) {
+                            c[j] = lds64(src + code_at + (4 * h + j) * raw_width);
+                            f[j] = lds_float(src + s_at + (4 * h + j) * s_pitch);
+                        }
+                        if (h == 1) {
+                            __syncwarp();                      // the warp has read the slot
+                            if (lane == 0)
+                                mbar_arrive(bar(bars.raw_empty[s]));
+                        } else if (!mbar_wait_bounded(bar(bars.empty[s]), phase ^ 1u, fault, kFaultWeightGrad)) {
+                            ok = false;
+                            break;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            sts128(dst + place[j] + h * 1024, decode8<CODE>(c[j], f[j]));
+                    }
+                    if (!ok)
+                        break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        cluster_arrive(full0 + s * 8);
                 }
                 if (++s == kStages) {
                     s = 0;
