@@ -59,9 +59,9 @@ struct WeightGradArgs {
     void *dw;
     const void *scale, *shift;                  // [hidden] of param_dtype, or null
     const float *dy_sum;                        // [out]
-    float *parts;                               // [splits][out][hidden] when splits > 1
+    float *parts;                               // weight_grad_part_bytes()
     int64_t rows, out, hidden;
-    int dtype, param_dtype, accumulate, block, code, splits;
+    int dtype, param_dtype, accumulate, block, code;
 };
 
 // Kernel attributes, once per device.
@@ -75,8 +75,8 @@ cudaError_t launch_norm_grad(int dtype, NormGradArgs *a, int sms, cudaStream_t s
 cudaError_t launch_gelu(int dtype, const GeluArgs &a, int sms, cudaStream_t stream);
 cudaError_t launch_gelu_grad(int dtype, GeluGradArgs *a, int sms, cudaStream_t stream);
 
-// Row splits of a weight gradient and the range its kernels address.
-int weight_grad_splits(int64_t rows, int64_t out, int64_t hidden);
+// Workspace of a weight gradient and the range its kernels address.
+int64_t weight_grad_part_bytes(int64_t rows, int64_t out, int64_t hidden);
 bool weight_grad_in_range(int64_t rows, int64_t out, int64_t hidden);
 cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
 

@@ -244,8 +244,7 @@ int64_t taco_weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden)
     if (check_elements(rows, hidden, &n) != TACO_OK || check_elements(rows, out, &n) != TACO_OK ||
         check_elements(out, hidden, &n) != TACO_OK)
         return -1;
-    const int splits = weight_grad_splits(rows, out, hidden);
-    return splits > 1 ? 4 * splits * n : 0;
+    return weight_grad_part_bytes(rows, out, hidden);
 }
 
 taco_status_t taco_weight_grad(const taco_weight_grad_args_t *a, taco_stream_t stream)
@@ -285,7 +284,7 @@ taco_status_t taco_weight_grad(const taco_weight_grad_args_t *a, taco_stream_t s
         return st;
     const WeightGradArgs k{a->dy, static_cast<const uint8_t *>(a->packed), a->dweight, a->scale, a->shift, a->dy_sum,
                            static_cast<float *>(a->workspace), a->rows, a->out, a->hidden, a->dtype, a->param_dtype,
-                           a->accumulate, a->block, a->code, weight_grad_splits(a->rows, a->out, a->hidden)};
+                           a->accumulate, a->block, a->code};
     return done(launch_weight_grad(k, dev->fault, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -294,19 +294,28 @@ __device__ __forceinline__ uint4 decode8(uint2 c, float f)
                       decode2<CODE>(c.y >> 16, f));
 }
 
-// Tiles of the grid's work: unit -> (split, tile row, tile column), columns fastest.
+// The grid's work.  Tiles go to the CTA pairs in order (columns fastest); the
+// last `tail` tiles, which would leave pairs idle, are cut into `splits` row
+// ranges each, whose sums go to `parts` and are joined by a second kernel.
 struct WgPlan {
-    int64_t units;
-    int tiles_m, tiles_n, stages_total, splits;
-    __device__ void at(int64_t u, int &m0, int &n0, int &split, int &first, int &count) const
+    int64_t units, whole;             // work items, and how many of them are whole tiles
+    int tiles_n, stages_total, tail, splits;
+    // part: index of the tile's sums in `parts`, or -1 for a whole tile
+    __device__ void at(int64_t u, int &m0, int &n0, int64_t &part, int &first, int &count) const
     {
-        const int64_t tiles = static_cast<int64_t>(tiles_m) * tiles_n;
-        split = static_cast<int>(u / tiles);
-        const int64_t t = u - split * tiles;
+        int64_t t = u;
+        first = 0;
+        count = stages_total;
+        part = -1;
+        if (u >= whole) {
+            part = u - whole;
+            const int split = static_cast<int>(part / tail);
+            t = whole + part - static_cast<int64_t>(split) * tail;
+            first = static_cast<int>(static_cast<int64_t>(stages_total) * split / splits);
+            count = static_cast<int>(static_cast<int64_t>(stages_total) * (split + 1) / splits) - first;
+        }
         m0 = static_cast<int>(t / tiles_n) * kPairM;
         n0 = static_cast<int>(t % tiles_n) * kPairN;
-        first = static_cast<int>(static_cast<int64_t>(stages_total) * split / splits);
-        count = static_cast<int>(static_cast<int64_t>(stages_total) * (split + 1) / splits) - first;
     }
 };
 
@@ -393,8 +402,9 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             uint32_t phase = 0, used = 0;
             bool ok = true;
             for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
-                int m0, n0, split, first, count;
-                plan.at(u, m0, n0, split, first, count);
+                int m0, n0, first, count;
+                int64_t part;
+                plan.at(u, m0, n0, part, first, count);
                 const int x = m0 + static_cast<int>(rank) * 128;
                 for (int k = first; k < first + count; k++) {
                     if (!mbar_wait_bounded_thread(bar(bars.empty[s]), phase ^ 1u, fault, kFaultWeightGrad)) {
@@ -421,8 +431,9 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             uint32_t phase = 0, chunk = 0;
             bool ok = true;
             for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
-                int m0, n0, split, first, count;
-                plan.at(u, m0, n0, split, first, count);
+                int m0, n0, first, count;
+                int64_t part;
+                plan.at(u, m0, n0, part, first, count);
                 for (int k = 0; k < count && ok; chunk++) {
                     const int b = static_cast<int>(chunk & 1);
                     if (chunk >= 2 && !cluster_wait(bar(bars.acc_empty[b]), ((chunk >> 1) - 1) & 1u, fault)) {
@@ -459,8 +470,9 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             uint32_t phase = 0, used = 0;
             bool ok = true;
             for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
-                int m0, n0, split, first, count;
-                plan.at(u, m0, n0, split, first, count);
+                int m0, n0, first, count;
+                int64_t part;
+                plan.at(u, m0, n0, part, first, count);
                 const RawSpan at(n0 + static_cast<int64_t>(rank) * 128, a.block, odd_shift);
                 for (int k = first; k < first + count; k++) {
                     if (!mbar_wait_bounded_thread(bar(bars.raw_empty[s]), phase ^ 1u, fault, kFaultWeightGrad)) {
@@ -493,8 +505,9 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             uint32_t phase = 0;
             bool ok = true;
             for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
-                int m0, n0, split, first, count;
-                plan.at(u, m0, n0, split, first, count);
+                int m0, n0, first, count;
+                int64_t part;
+                plan.at(u, m0, n0, part, first, count);
                 for (int k = 0; k < count; k++) {
                     if (!mbar_wait_bounded_thread(bar(bars.a_full[s]), phase, fault, kFaultWeightGrad)) {
                         ok = false;
@@ -531,8 +544,9 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
         uint32_t phase = 0;
         bool ok = true;
         for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
-            int m0, n0, split, first, count;
-            plan.at(u, m0, n0, split, first, count);
+            int m0, n0, first, count;
+                int64_t part;
+            plan.at(u, m0, n0, part, first, count);
             const RawSpan at(n0 + static_cast<int64_t>(rank) * 128, a.block, odd_shift);
             const uint32_t code_at = row_at + at.shift[sub] + col / span * (span + 8) + col % span;
             const uint32_t s_at = 4u + (a.block > 128 ? meta_row_at + at.meta_shift[sub]
@@ -587,8 +601,9 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
         int64_t chunk = 0;
         bool ok = true;
         for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
-            int m0, n0, split, first, count;
-            plan.at(u, m0, n0, split, first, count);
+            int m0, n0, first, count;
+                int64_t part;
+            plan.at(u, m0, n0, part, first, count);
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; i++)
@@ -615,15 +630,14 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                     cluster_arrive(empty0 + b * 8);
             }
             const int64_t m = m0 + static_cast<int64_t>(rank) * 128 + quarter * 32 + lane;
-            if (!ok || m >= a.out)
+            if (!ok || (m >= a.out && part < 0))
                 continue;
             const int64_t nbase = n0 + half * 128;
-            if (plan.splits > 1) {
-                float *to = a.parts + (split * a.out + m) * a.hidden + nbase;
+            if (part >= 0) {
+                float *to = a.parts + (part * kPairM + rank * 128 + quarter * 32 + lane) * kPairN + half * 128;
 #pragma unroll
                 for (int i = 0; i < 128; i += 4)
-                    if (nbase + i < a.hidden)
-                        *reinterpret_cast<float4 *>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                    *reinterpret_cast<float4 *>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
             } else {
                 const float sum = a.shift ? a.dy_sum[m] : 0.f;
 #pragma unroll
@@ -642,20 +656,23 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Adds the splits' sums in order and finishes four columns a thread.
-__global__ void __launch_bounds__(256) taco_weight_grad_join_kernel(WeightGradArgs a)
+// Adds the row ranges' sums of the last tiles in order and finishes four columns a thread.
+__global__ void __launch_bounds__(256) taco_weight_grad_join_kernel(WeightGradArgs a, WgPlan plan)
 {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int64_t n = a.out * a.hidden;
+    const int64_t n = static_cast<int64_t>(plan.tail) * kPairM * kPairN;
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n; i += 1024ll * gridDim.x) {
+        const int64_t t = plan.whole + i / (kPairM * kPairN);
+        const int64_t m = t / plan.tiles_n * kPairM + i / kPairN % kPairM, col = t % plan.tiles_n * kPairN + i % kPairN;
+        if (m >= a.out || col >= a.hidden)
+            continue;
         float4 v = *reinterpret_cast<const float4 *>(a.parts + i);
-        for (int s = 1; s < a.splits; s++) {
+        for (int s = 1; s < plan.splits; s++) {
             const float4 w = *reinterpret_cast<const float4 *>(a.parts + s * n + i);
             v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
         }
-        const int64_t m = i / a.hidden;
-        finish4(a, m, i - m * a.hidden, a.shift ? a.dy_sum[m] : 0.f, v);
+        finish4(a, m, col, a.shift ? a.dy_sum[m] : 0.f, v);
     }
 }
 
@@ -711,16 +728,33 @@ cudaError_t init_weight_grad()
     return e;
 }
 
-// Splits the rows where the tiles leave CTA pairs (of 76) idle, down to 512 rows a split.
-int weight_grad_splits(int64_t rows, int64_t out, int64_t hidden)
+// Tiles of a weight gradient, how many at the end are cut into row ranges, and
+// into how many.  76 pairs take the tiles in waves; what is left for the last
+// wave is cut so that all pairs have work, down to 512 rows a range: 8192 x 4096
+// x 4096 (256 tiles, 28 of them in the last wave) takes 197 us against 211 whole.
+constexpr int64_t kPairs = 76;
+
+struct WgTiles {
+    int64_t tiles, tail, splits;
+};
+
+WgTiles weight_grad_tiles(int64_t rows, int64_t out, int64_t hidden)
 {
-    if (!on_tensor_cores(out))
-        return 1;
-    const int64_t tiles = ((out + kPairM - 1) / kPairM) * ((hidden + kPairN - 1) / kPairN);
-    if (tiles == 0)
-        return 1;
-    const int64_t splits = std::min<int64_t>(76 / tiles, rows / 512);
-    return static_cast<int>(std::max<int64_t>(splits, 1));
+    WgTiles w{((out + kPairM - 1) / kPairM) * ((hidden + kPairN - 1) / kPairN), 0, 1};
+    if (!on_tensor_cores(out) || w.tiles == 0)
+        return w;
+    w.tail = w.tiles % kPairs;
+    if (w.tail > 0)
+        w.splits = std::max<int64_t>(1, std::min(kPairs / w.tail, rows / 512));
+    if (w.splits == 1)
+        w.tail = 0;
+    return w;
+}
+
+int64_t weight_grad_part_bytes(int64_t rows, int64_t out, int64_t hidden)
+{
+    const WgTiles w = weight_grad_tiles(rows, out, hidden);
+    return w.tail * w.splits * kPairM * kPairN * 4;
 }
 
 bool weight_grad_in_range(int64_t rows, int64_t out, int64_t hidden)
@@ -758,19 +792,20 @@ cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms
     }
     if (e != cudaSuccess)
         return e;
+    const WgTiles w = weight_grad_tiles(a.rows, a.out, a.hidden);
     WgPlan plan;
-    plan.tiles_m = static_cast<int>((a.out + kPairM - 1) / kPairM);
     plan.tiles_n = static_cast<int>((a.hidden + kPairN - 1) / kPairN);
     plan.stages_total = static_cast<int>((a.rows + kStageRows - 1) / kStageRows);
-    plan.splits = a.splits;
-    plan.units = static_cast<int64_t>(plan.tiles_m) * plan.tiles_n * a.splits;
+    plan.tail = static_cast<int>(w.tail);
+    plan.splits = static_cast<int>(w.splits);
+    plan.whole = w.tiles - w.tail;
+    plan.units = plan.whole + w.tail * w.splits;
     void *p[] = {&map, &raw, &args, &plan, &raw_width, &odd_shift, &odd_row0, &fault};
     e = launch_pairs(wg_kernel(a.code), static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
-    if (e == cudaSuccess && a.splits > 1) {
-        void *q[] = {&args};
-        const int64_t want = (a.out * a.hidden + 1023) / 1024;
+    if (e == cudaSuccess && plan.tail > 0) {
+        void *q[] = {&args, &plan};
         e = launch_kernel(reinterpret_cast<void *>(&taco_weight_grad_join_kernel),
-                          static_cast<int>(std::min<int64_t>(want, 8ll * sms)), 256, 0, stream, q);
+                          static_cast<int>(std::min<int64_t>(w.tail * 64, 8ll * sms)), 256, 0, stream, q);
     }
     return e;
 }
