@@ -59,7 +59,7 @@ struct WeightGradArgs {
     void *dw;
     const void *scale, *shift;                  // [hidden] of param_dtype, or null
     const float *dy_sum;                        // [out]
-    float *parts;                               // weight_grad_part_bytes()
+    float *parts;                               // weight_grad_workspace() bytes
     int64_t rows, out, hidden;
     int dtype, param_dtype, accumulate, block, code;
 };
@@ -76,7 +76,7 @@ cudaError_t launch_gelu(int dtype, const GeluArgs &a, int sms, cudaStream_t stre
 cudaError_t launch_gelu_grad(int dtype, GeluGradArgs *a, int sms, cudaStream_t stream);
 
 // Workspace of a weight gradient and the range its kernels address.
-int64_t weight_grad_part_bytes(int64_t rows, int64_t out, int64_t hidden);
+int64_t weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden);
 bool weight_grad_in_range(int64_t rows, int64_t out, int64_t hidden);
 cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
 

@@ -244,7 +244,7 @@ int64_t taco_weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden)
     if (check_elements(rows, hidden, &n) != TACO_OK || check_elements(rows, out, &n) != TACO_OK ||
         check_elements(out, hidden, &n) != TACO_OK)
         return -1;
-    return weight_grad_part_bytes(rows, out, hidden);
+    return weight_grad_workspace(rows, out, hidden);
 }
 
 taco_status_t taco_weight_grad(const taco_weight_grad_args_t *a, taco_stream_t stream)

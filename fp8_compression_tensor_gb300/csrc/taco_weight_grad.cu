@@ -42,8 +42,6 @@
 namespace taco {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
-
 __device__ __forceinline__ void finish_element(const WeightGradArgs &a, int64_t m, int64_t n, float v)
 {
     if (a.scale)
@@ -90,50 +88,34 @@ __device__ __forceinline__ void finish4(const WeightGradArgs &a, int64_t m, int6
     }
 }
 
-// ---------------------------------------------------------------------------
-// Output widths that are no multiple of 8 (dY's rows are then not 16-byte
-// aligned, which TMA needs): CUDA cores
-// ---------------------------------------------------------------------------
-
-// 64 x 64 tiles of dW, 4 x 4 values a thread.
-__global__ void __launch_bounds__(256) taco_weight_grad_any_kernel(WeightGradArgs a)
+// dW of no rows: four columns a thread.
+__global__ void __launch_bounds__(256) taco_weight_grad_empty_kernel(WeightGradArgs a)
 {
-    __shared__ float sa[kDepth][kTile], sb[kDepth][kTile];
     grid_launch_dependents();
     grid_dependency_wait();
-    const int64_t across = (a.hidden + kTile - 1) / kTile;
-    const int64_t m0 = blockIdx.x / across * kTile, n0 = blockIdx.x % across * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const __nv_bfloat16 *dy = static_cast<const __nv_bfloat16 *>(a.dy);
-    float acc[4][4] = {};
-    for (int64_t r0 = 0; r0 < a.rows; r0 += kDepth) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kDepth * kTile; i += 256) {
-            const int64_t r = r0 + i / kTile, m = m0 + i % kTile, n = n0 + i % kTile;
-            sa[i / kTile][i % kTile] = r < a.rows && m < a.out ? __bfloat162float(dy[r * a.out + m]) : 0.f;
-            sb[i / kTile][i % kTile] =
-                r < a.rows && n < a.hidden ? record_value(a.packed, r * a.hidden + n, a.block, a.code) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; k++) {
-            float x[4], y[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                x[j] = sa[k][ty * 4 + j];
-                y[j] = sb[k][tx * 4 + j];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-        }
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < a.out * a.hidden; i += 1024ll * gridDim.x) {
+        const int64_t m = i / a.hidden;
+        finish4(a, m, i - m * a.hidden, a.shift ? a.dy_sum[m] : 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
     }
-    for (int i = 0; i < 4; i++)
-        for (int j = 0; j < 4; j++)
-            if (m0 + ty * 4 + i < a.out && n0 + tx * 4 + j < a.hidden)
-                finish_element(a, m0 + ty * 4 + i, n0 + tx * 4 + j, acc[i][j]);
+}
+
+// dY with rows of a multiple of 8 elements: TMA reads rows of whole 16 bytes, so
+// where `out` is no multiple of 8 the rows are first copied `width` elements
+// apart (zeros behind each), eight elements a thread.
+__global__ void __launch_bounds__(256) taco_weight_grad_widen_kernel(const uint16_t *dy, int64_t rows, int64_t out, int64_t width, uint4 *to)
+{
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t vectors = width / 8, n = rows * vectors;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += 256ll * gridDim.x) {
+        const int64_t r = i / vectors, c = (i - r * vectors) * 8;
+        const uint16_t *src = dy + r * out + c;
+        uint32_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            v[k] = c + k < out ? src[k] : 0u;
+        to[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -715,9 +697,6 @@ cudaError_t encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *ba
                : cudaErrorInvalidValue;
 }
 
-// The tensor-core kernel's TMA view of dY needs rows of a multiple of 16 bytes.
-bool on_tensor_cores(int64_t out) { return out % 8 == 0; }
-
 }  // namespace
 
 cudaError_t init_weight_grad()
@@ -741,8 +720,6 @@ struct WgTiles {
 WgTiles weight_grad_tiles(int64_t rows, int64_t out, int64_t hidden)
 {
     WgTiles w{((out + kPairM - 1) / kPairM) * ((hidden + kPairN - 1) / kPairN), 0, 1};
-    if (!on_tensor_cores(out) || w.tiles == 0)
-        return w;
     w.tail = w.tiles % kPairs;
     if (w.tail > 0)
         w.splits = std::max<int64_t>(1, std::min(kPairs / w.tail, rows / 512));
@@ -751,25 +728,41 @@ WgTiles weight_grad_tiles(int64_t rows, int64_t out, int64_t hidden)
     return w;
 }
 
-int64_t weight_grad_part_bytes(int64_t rows, int64_t out, int64_t hidden)
+// The row ranges' sums, then dY in rows of a multiple of 8 where it has others.
+int64_t weight_grad_part_bytes(const WgTiles &w) { return w.tail * w.splits * kPairM * kPairN * 4; }
+
+int64_t weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden)
 {
-    const WgTiles w = weight_grad_tiles(rows, out, hidden);
-    return w.tail * w.splits * kPairM * kPairN * 4;
+    return weight_grad_part_bytes(weight_grad_tiles(rows, out, hidden)) + (out % 8 ? 2 * rows * ((out + 7) / 8 * 8) : 0);
 }
 
 bool weight_grad_in_range(int64_t rows, int64_t out, int64_t hidden)
 {
     // 32-bit TMA coordinates, whole tiles and stages past the end included
-    return rows <= INT32_MAX - 64 && out <= INT32_MAX - 256 && hidden <= INT32_MAX / 2 && (out + kTile - 1) / kTile <= INT32_MAX / ((hidden + kTile - 1) / kTile + 1);
+    return rows <= INT32_MAX - 64 && out <= INT32_MAX - 256 && hidden <= INT32_MAX / 2;
 }
 
 cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream)
 {
     WeightGradArgs args = a;
-    if (!on_tensor_cores(a.out) || a.rows == 0) {
+    if (a.rows == 0) {
         void *p[] = {&args};
-        const int64_t tiles = (a.hidden + kTile - 1) / kTile * ((a.out + kTile - 1) / kTile);
-        return launch_kernel(reinterpret_cast<void *>(&taco_weight_grad_any_kernel), static_cast<int>(tiles), 256, 0, stream, p);
+        return launch_kernel(reinterpret_cast<void *>(&taco_weight_grad_empty_kernel),
+                             static_cast<int>(std::min<int64_t>((a.out * a.hidden + 1023) / 1024, 8ll * sms)), 256, 0, stream, p);
+    }
+    const WgTiles w = weight_grad_tiles(a.rows, a.out, a.hidden);
+    int64_t width = (a.out + 7) / 8 * 8;
+    const void *dy = a.dy;
+    if (width != a.out) {
+        void *to = reinterpret_cast<uint8_t *>(a.parts) + weight_grad_part_bytes(w);
+        int64_t rows = a.rows, out = a.out;
+        void *p[] = {&dy, &rows, &out, &width, &to};
+        const cudaError_t e = launch_kernel(reinterpret_cast<void *>(&taco_weight_grad_widen_kernel),
+                                            static_cast<int>(std::min<int64_t>((rows * width + 2047) / 2048, 8ll * sms)), 256, 0,
+                                            stream, p);
+        if (e != cudaSuccess)
+            return e;
+        dy = to;
     }
     alignas(64) CUtensorMap map;
     alignas(64) RawMaps raw;
@@ -780,7 +773,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms
     const int64_t even_rows = (a.rows + 1) / 2, odd_rows = a.rows / 2;
     int odd_row0 = odd_rows ? 0 : 1;   // a single row: the odd map holds it too, read from row 1 on, which is outside
     const uint8_t *odd_base = odd_rows ? a.packed + pitch - odd_shift : a.packed;
-    cudaError_t e = encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.dy, a.out, a.rows, 2 * a.out, 64, kStageRows,
+    cudaError_t e = encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, a.out, a.rows, 2 * width, 64, kStageRows,
                               CU_TENSOR_MAP_SWIZZLE_128B);
     for (int i = 0; i < 2 && e == cudaSuccess; i++) {
         const int width = i ? 16 : raw_width;
@@ -792,7 +785,6 @@ cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms
     }
     if (e != cudaSuccess)
         return e;
-    const WgTiles w = weight_grad_tiles(a.rows, a.out, a.hidden);
     WgPlan plan;
     plan.tiles_n = static_cast<int>((a.hidden + kPairN - 1) / kPairN);
     plan.stages_total = static_cast<int>((a.rows + kStageRows - 1) / kStageRows);
