@@ -42,16 +42,25 @@
 namespace taco {
 namespace {
 
-__device__ __forceinline__ void finish_element(const WeightGradArgs &a, int64_t m, int64_t n, float v)
+__device__ __forceinline__ void store4(float *to, float4 v, int accumulate)
 {
-    if (a.scale)
-        v *= load_param(a.scale, a.param_dtype, n);
-    if (a.shift)
-        v = fmaf(a.dy_sum[m], load_param(a.shift, a.param_dtype, n), v);
-    const int64_t i = m * a.hidden + n;
-    if (a.accumulate)
-        v += load_param(a.dw, a.dtype, i);
-    store_param(a.dw, a.dtype, i, v);
+    float4 *p = reinterpret_cast<float4 *>(to);
+    if (accumulate) {
+        const float4 w = *p;
+        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    }
+    *p = v;
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *to, float4 v, int accumulate)
+{
+    uint2 *p = reinterpret_cast<uint2 *>(to);
+    if (accumulate) {
+        const uint2 w = *p;
+        v = make_float4(v.x + __uint_as_float(w.x << 16), v.y + __uint_as_float(w.x & 0xffff0000u),
+                        v.z + __uint_as_float(w.y << 16), v.w + __uint_as_float(w.y & 0xffff0000u));
+    }
+    *p = make_uint2(float2_to_bf16x2(v.x, v.y), float2_to_bf16x2(v.z, v.w));
 }
 
 // Four columns of row m; sum = dy_sum[m].
@@ -70,22 +79,10 @@ __device__ __forceinline__ void finish4(const WeightGradArgs &a, int64_t m, int6
         v.w = fmaf(sum, load_param(a.shift, a.param_dtype, n + 3), v.w);
     }
     const int64_t i = m * a.hidden + n;
-    if (a.dtype == kTypeF32) {
-        float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(a.dw) + i);
-        if (a.accumulate) {
-            const float4 w = *to;
-            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-        }
-        *to = v;
-    } else {
-        uint2 *to = reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.dw) + i);
-        if (a.accumulate) {
-            const uint2 w = *to;
-            v = make_float4(v.x + __uint_as_float(w.x << 16), v.y + __uint_as_float(w.x & 0xffff0000u),
-                            v.z + __uint_as_float(w.y << 16), v.w + __uint_as_float(w.y & 0xffff0000u));
-        }
-        *to = make_uint2(float2_to_bf16x2(v.x, v.y), float2_to_bf16x2(v.z, v.w));
-    }
+    if (a.dtype == kTypeF32)
+        store4(static_cast<float *>(a.dw) + i, v, a.accumulate);
+    else
+        store4(static_cast<__nv_bfloat16 *>(a.dw) + i, v, a.accumulate);
 }
 
 // dW of no rows: four columns a thread.
@@ -132,7 +129,7 @@ constexpr int kTeam = 4;                                         // decoder warp
 constexpr int kRawWidth = 176;                                   // widest box of record bytes: 4 records of B = 32, and 8 bytes of slack
 constexpr int kRawBytes = kStageRows * (kRawWidth + 16);         // even rows, odd rows, then their scales where they lie apart
 constexpr int kWgThreads = 640;
-constexpr size_t kWgSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOperandBytes + kStages * kRawBytes + 512;
+constexpr size_t kWgSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOperandBytes + kStages * kRawBytes;
 constexpr uint32_t kIdesc = mma_idesc_bf16_f32(kPairM, kPairN) | (1u << 15) | (1u << 16);   // A and B MN-major
 
 struct WgBarriers {
@@ -276,6 +273,22 @@ __device__ __forceinline__ uint4 decode8(uint2 c, float f)
                       decode2<CODE>(c.y >> 16, f));
 }
 
+// Writes a thread's 128 columns of a row, `left` of which exist: sums scale + sum
+// shift, `affine` holding 128 scales and, 256 floats on, the shifts.  The types of
+// scale and shift are dealt with before: with their conversions in this unrolled
+// loop 8192 x 16384 x 4096 with scale and shift took 802 us, without 748.
+template <typename T>
+__device__ __forceinline__ void finish_row(const float (&acc)[128], const float *affine, float sum, T *to, int64_t left, int accumulate)
+{
+#pragma unroll
+    for (int i = 0; i < 128; i += 4)
+        if (i < left) {
+            const float4 s = *reinterpret_cast<const float4 *>(affine + i), t = *reinterpret_cast<const float4 *>(affine + 256 + i);
+            store4(to + i, make_float4(fmaf(sum, t.x, acc[i] * s.x), fmaf(sum, t.y, acc[i + 1] * s.y),
+                                       fmaf(sum, t.z, acc[i + 2] * s.z), fmaf(sum, t.w, acc[i + 3] * s.w)), accumulate);
+        }
+}
+
 // The grid's work.  Tiles go to the CTA pairs in order (columns fastest); the
 // last `tail` tiles, which would leave pairs idle, are cut into `splits` row
 // ranges each, whose sums go to `parts` and are joined by a second kernel.
@@ -339,6 +352,7 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) WgBarriers bars;
+    __shared__ __align__(16) float affine[512];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t raw = base + kStages * 2 * kOperandBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -612,21 +626,29 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                     cluster_arrive(empty0 + b * 8);
             }
             const int64_t m = m0 + static_cast<int64_t>(rank) * 128 + quarter * 32 + lane;
-            if (!ok || (m >= a.out && part < 0))
-                continue;
             const int64_t nbase = n0 + half * 128;
             if (part >= 0) {
                 float *to = a.parts + (part * kPairM + rank * 128 + quarter * 32 + lane) * kPairN + half * 128;
+                if (ok)
 #pragma unroll
-                for (int i = 0; i < 128; i += 4)
-                    *reinterpret_cast<float4 *>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-            } else {
-                const float sum = a.shift ? a.dy_sum[m] : 0.f;
-#pragma unroll
-                for (int i = 0; i < 128; i += 4)
-                    if (nbase + i < a.hidden)
-                        finish4(a, m, nbase + i, sum, make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]));
+                    for (int i = 0; i < 128; i += 4)
+                        *reinterpret_cast<float4 *>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                continue;
             }
+            // scale and shift of the tile's 256 columns as binary32 in shared memory
+            const int c = threadIdx.x - (4 + 2 * kTeam) * 32;
+            named_barrier_sync(1, 256);                        // the last tile's have been read
+            affine[c] = a.scale && n0 + c < a.hidden ? load_param(a.scale, a.param_dtype, n0 + c) : 1.f;
+            affine[256 + c] = a.shift && n0 + c < a.hidden ? load_param(a.shift, a.param_dtype, n0 + c) : 0.f;
+            named_barrier_sync(1, 256);
+            if (!ok || m >= a.out)
+                continue;
+            const float sum = a.shift ? a.dy_sum[m] : 0.f;
+            if (a.dtype == kTypeF32)
+                finish_row(acc, affine + half * 128, sum, static_cast<float *>(a.dw) + m * a.hidden + nbase, a.hidden - nbase, a.accumulate);
+            else
+                finish_row(acc, affine + half * 128, sum, static_cast<__nv_bfloat16 *>(a.dw) + m * a.hidden + nbase, a.hidden - nbase,
+                           a.accumulate);
         }
     }
     tc_fence_before_sync();
