@@ -7,6 +7,7 @@ every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -110,8 +111,19 @@ def _check(rc: int, what: str):
         raise TacoError(rc, what, detail)
 
 
+_current_device = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_device(device: torch.device):
+    """Context of the device; nothing to do where it is the current one."""
+    return _current_device if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
 def _stream_handle(device: torch.device, stream) -> int:
     if stream is None:
+        if _raw_stream is not None and device.index is not None:
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -160,7 +172,7 @@ def compress(x: torch.Tensor, block: int = 128, out: Optional[torch.Tensor] = No
         if out.numel() != nbytes:
             raise ValueError(f"out must have {nbytes} bytes, has {out.numel()}")
     opt = _options(block, variant, code)
-    with torch.cuda.device(x.device):
+    with _on_device(x.device):
         if opt is None:
             rc = load_library().taco_compress(x.data_ptr(), rows, hidden, block, out.data_ptr(),
                                               _stream_handle(x.device, stream))
@@ -186,7 +198,7 @@ def decompress(packed: torch.Tensor, rows: int, hidden: int, block: int = 128,
         if out.numel() != rows * hidden:
             raise ValueError("out has the wrong number of elements")
     opt = _options(block, variant, code)
-    with torch.cuda.device(packed.device):
+    with _on_device(packed.device):
         if opt is None:
             rc = load_library().taco_decompress(packed.data_ptr(), rows, hidden, block, out.data_ptr(),
                                                 _stream_handle(packed.device, stream))
@@ -218,7 +230,7 @@ def reduce_shards(shards: Sequence[torch.Tensor], rows: int, hidden: int, block:
             raise ValueError(f"out must have {nbytes} bytes")
     ptrs = (ctypes.c_void_p * len(shards))(*[s.data_ptr() for s in shards])
     opt = _options(block, variant, code)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         if opt is None:
             rc = load_library().taco_reduce_shards(ptrs, len(shards), rows, hidden, block, out.data_ptr(),
                                                    _stream_handle(dev, stream))
@@ -235,7 +247,7 @@ def selftest_encode_bits(code, first: int, out: torch.Tensor, stream=None) -> to
     (taco_selftest_encode_bits)."""
     _check_cuda_tensor(out, torch.uint8, "out")
     c = CODES[code] if isinstance(code, str) else int(code)
-    with torch.cuda.device(out.device):
+    with _on_device(out.device):
         rc = load_library().taco_selftest_encode_bits(c, first & 0xFFFFFFFF, out.numel(), out.data_ptr(),
                                                       _stream_handle(out.device, stream))
     _check(rc, "taco_selftest_encode_bits")

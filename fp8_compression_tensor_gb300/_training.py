@@ -22,7 +22,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import CODES, _check, compressed_bytes, load_library
+from ._binding import CODES, _check, _raw_stream, compressed_bytes, load_library
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _i64, _i32, _f32, _ptr = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p
@@ -165,9 +165,6 @@ def _param_type(t, name: str):
 
 def _packed(packed, rows: int, hidden: int, block: int, device: int) -> int:
     return _tensor(packed, "packed", device, torch.uint8, (compressed_bytes(rows, hidden, block),))
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _run(device: int, stream, call):
