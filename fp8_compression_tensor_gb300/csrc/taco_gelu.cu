@@ -78,9 +78,10 @@ __device__ __forceinline__ float2 tanh_gate2(float2 u)
     return make_float2(reciprocal_fast(1.f + exp2_fast(x.x)), reciprocal_fast(1.f + exp2_fast(x.y)));
 }
 
-__device__ __forceinline__ float2 gelu_value2(float2 u, int tanh_form)
+template <bool TANH>
+__device__ __forceinline__ float2 gelu_value2(float2 u)
 {
-    if (tanh_form)
+    if (TANH)
         return mul2(u, tanh_gate2(u));
     float2 e;
     const float2 a = make_float2(bounded_abs(u.x), bounded_abs(u.y));
@@ -95,9 +96,10 @@ __device__ __forceinline__ float with_sign_of(float v, float u)
 }
 
 // gelu(u) and its slope.
-__device__ __forceinline__ void gelu_both2(float2 u, int tanh_form, float2 &y, float2 &slope)
+template <bool TANH>
+__device__ __forceinline__ void gelu_both2(float2 u, float2 &y, float2 &slope)
 {
-    if (tanh_form) {
+    if (TANH) {
         const float2 g = tanh_gate2(u);
         // Beyond |u| = 16 the gate is 0 or 1 and its slope 0; the clamp keeps u^2 finite.
         const float2 c = make_float2(fminf(fmaxf(u.x, -16.f), 16.f), fminf(fmaxf(u.y, -16.f), 16.f));
@@ -124,7 +126,8 @@ __device__ __forceinline__ void gelu_both2(float2 u, int tanh_form, float2 &y, f
 
 // Whole vectors of eight: a warp takes 512 consecutive elements at a time, two
 // vectors a lane (the layout of block_max), with the next ones' loads in flight.
-template <typename T>
+// CODE: code format of the records, or -1 for none.
+template <typename T, bool TANH, int CODE>
 __global__ void __launch_bounds__(256, 4) taco_gelu_kernel(GeluArgs a)
 {
     grid_launch_dependents();
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(256, 4) taco_gelu_kernel(GeluArgs a)
     // Column of the first vector, kept up by adding the step modulo the width.
     const int C = static_cast<int>(a.hidden), col_step = static_cast<int>(step % C), col_next = 256 % C;
     int col = static_cast<int>(at % C);
-    const int shift = a.packed ? 31 - __clz(a.block) : 0;
+    const int shift = CODE >= 0 ? 31 - __clz(a.block) : 0;
     grid_dependency_wait();
     Raw8<T> next[2];
     auto fetch = [&](int64_t i) {
@@ -171,10 +174,10 @@ __global__ void __launch_bounds__(256, 4) taco_gelu_kernel(GeluArgs a)
                 F8 y;
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    y.v[i] = gelu_value2(u[j].v[i], a.tanh_form);
+                    y.v[i] = gelu_value2<TANH>(u[j].v[i]);
                 store_raw8(static_cast<T *>(a.y) + at + 256 * j, pack<T>(y));
             }
-        if (a.packed) {
+        if (CODE >= 0) {
             uint32_t top[2] = {block_max(u[0], a.block), block_max(u[1], a.block)};
             if (a.block == 512)
                 top[0] = top[1] = max(top[0], top[1]);
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(256, 4) taco_gelu_kernel(GeluArgs a)
             for (int j = 0; j < 2; j++) {
                 const int64_t i = at + 256 * j;
                 if (i < n)
-                    write_codes(u[j], top[j], a.packed + i + (i >> shift) * 8, static_cast<int>(i & (a.block - 1)), a.block, a.code);
+                    write_codes<CODE>(u[j], top[j], a.packed + i + (i >> shift) * 8, static_cast<int>(i & (a.block - 1)), a.block);
             }
         }
     }
@@ -199,7 +202,8 @@ __global__ void __launch_bounds__(256) taco_gelu_any_kernel(GeluArgs a)
         float u = to_float(static_cast<const T *>(a.x)[i]);
         if (a.bias)
             u += load_param(a.bias, a.param_dtype, i % a.hidden);
-        static_cast<T *>(a.y)[i] = from_float<T>(gelu_value2(make_float2(u, u), a.tanh_form).x);
+        const float2 y = a.tanh_form ? gelu_value2<true>(make_float2(u, u)) : gelu_value2<false>(make_float2(u, u));
+        static_cast<T *>(a.y)[i] = from_float<T>(y.x);
     }
 }
 
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(256) taco_gelu_any_kernel(GeluArgs a)
 // end.  The next row's loads are in flight.
 constexpr int kGradThreads = 512;
 
-template <typename T>
+template <typename T, bool TANH, int CODE>
 __global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGradArgs a, int strip)
 {
     __shared__ float part[kGradThreads * 8];
@@ -240,14 +244,17 @@ __global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGra
     fetch(row);
     if (in)
         for (; row < a.rows; row += step) {
-            const F8 g = unpack(next_dy), q = codes8_to_float(next_codes, a.code);
+            const F8 g = unpack(next_dy), q = codes8_to_float(next_codes, CODE);
             const float s = next_s;
             fetch(row + step);
-            F8 d, y;
+            F8 d, y = {};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                float2 slope;
-                gelu_both2(mul2(q.v[i], both(s)), a.tanh_form, y.v[i], slope);
+                float2 slope = both(0.f);
+                // The second condition always holds.  As a branch it keeps the compiler from interleaving the four pairs of the
+                // erf form, which ran 8192 x 16384 in 177 us; one after the other they take 162.
+                if (TANH || a.tanh_form == 0)
+                    gelu_both2<TANH>(mul2(q.v[i], both(s)), y.v[i], slope);
                 d.v[i] = mul2(g.v[i], slope);
                 db.v[i] = add2(db.v[i], d.v[i]);
             }
@@ -275,6 +282,23 @@ __global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGra
     }
 }
 
+template <typename T, bool TANH>
+const void *gelu_kernel(int code)
+{
+    return code < 0    ? reinterpret_cast<void *>(&taco_gelu_kernel<T, TANH, -1>)
+           : code == 0 ? reinterpret_cast<void *>(&taco_gelu_kernel<T, TANH, 0>)
+           : code == 1 ? reinterpret_cast<void *>(&taco_gelu_kernel<T, TANH, 1>)
+                       : reinterpret_cast<void *>(&taco_gelu_kernel<T, TANH, 2>);
+}
+
+template <typename T, bool TANH>
+const void *gelu_grad_kernel(int code)
+{
+    return code == 0   ? reinterpret_cast<void *>(&taco_gelu_grad_kernel<T, TANH, 0>)
+           : code == 1 ? reinterpret_cast<void *>(&taco_gelu_grad_kernel<T, TANH, 1>)
+                       : reinterpret_cast<void *>(&taco_gelu_grad_kernel<T, TANH, 2>);
+}
+
 template <typename T>
 cudaError_t gelu(const GeluArgs &a, int sms, cudaStream_t stream)
 {
@@ -285,8 +309,11 @@ cudaError_t gelu(const GeluArgs &a, int sms, cudaStream_t stream)
         const int64_t want = (n + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
         return launch_kernel(reinterpret_cast<void *>(&taco_gelu_any_kernel<T>), static_cast<int>(std::min(want, cap)), 256, 0, stream, p);
     }
-    const int64_t want = (n + 4095) / 4096, cap = static_cast<int64_t>(sms) * 4;
-    return launch_kernel(reinterpret_cast<void *>(&taco_gelu_kernel<T>), static_cast<int>(std::min(want, cap)), 256, 0, stream, p);
+    // Four waves: CTAs that finish early make room (one wave runs 8192 x 16384 with records 6 us longer).
+    const int64_t want = (n + 4095) / 4096, cap = static_cast<int64_t>(sms) * 16;
+    const int code = a.packed ? a.code : -1;
+    return launch_kernel(a.tanh_form ? gelu_kernel<T, true>(code) : gelu_kernel<T, false>(code),
+                         static_cast<int>(std::min(want, cap)), 256, 0, stream, p);
 }
 
 // Row chunks for a grid of `strips` columns of CTAs: the fewest (up to eight
@@ -321,7 +348,8 @@ cudaError_t gelu_grad(GeluGradArgs *a, int sms, cudaStream_t stream)
     const int64_t rows_a_pass = kGradThreads / strip, passes = (a->rows + rows_a_pass - 1) / rows_a_pass;
     a->nparts = row_chunks(strips, passes, 2 * sms);
     void *p[] = {a, &strip};
-    return launch_kernel_2d(reinterpret_cast<void *>(&taco_gelu_grad_kernel<T>), static_cast<unsigned>(strips),
+    return launch_kernel_2d(a->tanh_form ? gelu_grad_kernel<T, true>(a->code) : gelu_grad_kernel<T, false>(a->code),
+                            static_cast<unsigned>(strips),
                             static_cast<unsigned>(a->nparts), kGradThreads, 0, stream, p);
 }
 

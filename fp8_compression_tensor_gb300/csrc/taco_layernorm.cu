@@ -241,8 +241,15 @@ __global__ void __launch_bounds__(kNormThreads, 1) taco_norm_kernel(NormArgs a, 
                 }
                 store_raw8(static_cast<T *>(a.y) + row * C + col[j], pack<T>(y));
             }
-        if (a.packed)
-            write_records<NV>(h, col, C, a.packed + row * (C / a.block) * (a.block + 8), a.block, a.code);
+        if (a.packed) {
+            uint8_t *to = a.packed + row * (C / a.block) * (a.block + 8);
+            if (a.code == 0)
+                write_records<NV, 0>(h, col, C, to, a.block);
+            else if (a.code == 1)
+                write_records<NV, 1>(h, col, C, to, a.block);
+            else
+                write_records<NV, 2>(h, col, C, to, a.block);
+        }
     }
 }
 

@@ -283,22 +283,21 @@ __device__ __forceinline__ uint32_t block_max(const F8 &u, int block)
 
 // Writes this lane's codes to `at` and, from the lane that holds the block's
 // last ones, (1, s) behind them.  `from`: first element's place in the block.
-__device__ __forceinline__ void write_codes(const F8 &u, uint32_t top, uint8_t *at, int from, int block, int code)
+template <int CODE>
+__device__ __forceinline__ void write_codes(const F8 &u, uint32_t top, uint8_t *at, int from, int block)
 {
     float inv;
-    const float s = record_scale(top, code, &inv);
-    uint2 q = make_uint2(0u, 0u);
-    if (inv != 0.f)
-        q = make_uint2(encode4_scaled(code, u.v[0], u.v[1], inv), encode4_scaled(code, u.v[2], u.v[3], inv));
-    *reinterpret_cast<uint2 *>(at) = q;
+    const float s = record_scale(top, CODE, &inv);
+    const uint2 q = make_uint2(encode4_scaled(CODE, u.v[0], u.v[1], inv), encode4_scaled(CODE, u.v[2], u.v[3], inv));
+    *reinterpret_cast<uint2 *>(at) = inv == 0.f ? make_uint2(0u, 0u) : q;
     if (from + 8 == block)
         *reinterpret_cast<float2 *>(at + 8) = make_float2(1.f, s);
 }
 
 // Records of NV vectors of eight a lane, vector j starting at column col[j] of a
 // row of C; `row` is the row's first record byte.
-template <int NV>
-__device__ __forceinline__ void write_records(const F8 (&u)[NV], const int (&col)[NV], int C, uint8_t *row, int block, int code)
+template <int NV, int CODE>
+__device__ __forceinline__ void write_records(const F8 (&u)[NV], const int (&col)[NV], int C, uint8_t *row, int block)
 {
     uint32_t top[NV];
 #pragma unroll
@@ -313,7 +312,7 @@ __device__ __forceinline__ void write_records(const F8 (&u)[NV], const int (&col
 #pragma unroll
     for (int j = 0; j < NV; j++)
         if (col[j] < C)
-            write_codes(u[j], top[j], row + col[j] + (col[j] >> shift) * 8, col[j] & (block - 1), block, code);
+            write_codes<CODE>(u[j], top[j], row + col[j] + (col[j] >> shift) * 8, col[j] & (block - 1), block);
 }
 
 // Byte of element `col` in a record row.
