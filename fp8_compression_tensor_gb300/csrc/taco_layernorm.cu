@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) taco_norm_kernel(NormArgs a, 
 #pragma unroll
                     for (int k = 0; k < kUnits; k++, to += unit)
                         if (FULL || col[j] < C)
-                            copy16(to, reinterpret_cast<const uint4 *>(src + row * C + col[j]) + k);
+                            copy16<T>(to, reinterpret_cast<const uint4 *>(src + row * C + col[j]) + k);
             };
             piece(x);
             if (res)

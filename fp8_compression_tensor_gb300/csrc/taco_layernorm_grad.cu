@@ -120,7 +120,7 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
 #pragma unroll
                     for (int k = 0; k < kUnits; k++, to += unit)
                         if (FULL || col[j] < C)
-                            copy16(to, reinterpret_cast<const uint4 *>(static_cast<const T *>(src) + row * C + col[j]) + k);
+                            copy16<T>(to, reinterpret_cast<const uint4 *>(static_cast<const T *>(src) + row * C + col[j]) + k);
             };
             piece(a.dy);
             if (!RECORDS)
