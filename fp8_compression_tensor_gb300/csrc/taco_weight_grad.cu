@@ -122,14 +122,16 @@ __global__ void __launch_bounds__(256) taco_weight_grad_widen_kernel(const uint1
 constexpr int kPairM = 256, kPairN = 256;     // tile of a CTA pair; each CTA holds 128 rows of A and of B
 constexpr int kStageRows = 64;                // rows of dY and X per pipeline stage
 constexpr int kChunkRows = 1024;              // rows per tensor-core accumulation
-constexpr int kStages = 5;                    // of both operands and of the record bytes
+constexpr int kStages = 4;                    // of both operands and of the record bytes
 constexpr int kOperandBytes = 128 * kStageRows * 2;             // one CTA's A or B of a stage
 constexpr int kHalfBytes = 64 * kStageRows * 2;                 // 64 columns of it
 constexpr int kTeam = 4;                                         // decoder warps of a stage, 16 rows each; two teams
 constexpr int kRawWidth = 176;                                   // widest box of record bytes: 4 records of B = 32, and 8 bytes of slack
 constexpr int kRawBytes = kStageRows * (kRawWidth + 16);         // even rows, odd rows, then their scales where they lie apart
+// Columns that a warp of the epilogue turns round at a time, and its buffer.
+constexpr int kTurnColumns = 32, kTurnBytes = 32 * kTurnColumns * 4;
 constexpr int kWgThreads = 640;
-constexpr size_t kWgSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOperandBytes + kStages * kRawBytes;
+constexpr size_t kWgSmem = 1024 + static_cast<size_t>(kStages) * 2 * kOperandBytes + kStages * kRawBytes + 8 * kTurnBytes;
 constexpr uint32_t kIdesc = mma_idesc_bf16_f32(kPairM, kPairN) | (1u << 15) | (1u << 16);   // A and B MN-major
 
 struct WgBarriers {
@@ -229,13 +231,6 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
         : "memory");
 }
 
-__device__ __forceinline__ float lds_float(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
-
 // 16 consecutive tensor-memory columns of this thread's lane, complete on return.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -273,20 +268,46 @@ __device__ __forceinline__ uint4 decode8(uint2 c, float f)
                       decode2<CODE>(c.y >> 16, f));
 }
 
-// Writes a thread's 128 columns of a row, `left` of which exist: sums scale + sum
-// shift, `affine` holding 128 scales and, 256 floats on, the shifts.  The types of
-// scale and shift are dealt with before: with their conversions in this unrolled
-// loop 8192 x 16384 x 4096 with scale and shift took 802 us, without 748.
-template <typename T>
-__device__ __forceinline__ void finish_row(const float (&acc)[128], const float *affine, float sum, T *to, int64_t left, int accumulate)
+__device__ __forceinline__ float lds_float(uint32_t addr)
 {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ float4 lds_float4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+// Writes a warp's sums, a row of 128 columns a lane: 32 columns at a time go
+// through the warp's shared-memory buffer (16-byte units swizzled by the row), so
+// that eight lanes then write 128 consecutive bytes of a row.  Written straight
+// from the registers, 16 bytes to each of 32 rows an instruction, they kept the
+// load/store unit busy for 32 cycles an instruction, which the decoders need too:
+// 8192 x 16384 x 4096 took 715 us, turned 686, and 1024^3 16.2 us against 13.0.
+// `put(row, col, v)` takes four columns.
+template <typename Put>
+__device__ __forceinline__ void write_turned(const float (&acc)[128], uint32_t buffer, Put put)
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 128; i += 4)
-        if (i < left) {
-            const float4 s = *reinterpret_cast<const float4 *>(affine + i), t = *reinterpret_cast<const float4 *>(affine + 256 + i);
-            store4(to + i, make_float4(fmaf(sum, t.x, acc[i] * s.x), fmaf(sum, t.y, acc[i + 1] * s.y),
-                                       fmaf(sum, t.z, acc[i + 2] * s.z), fmaf(sum, t.w, acc[i + 3] * s.w)), accumulate);
+    for (int c = 0; c < 128; c += kTurnColumns) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kTurnColumns / 4; i++)
+            sts128(buffer + lane * 128 + ((i ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(acc[c + 4 * i]), __float_as_uint(acc[c + 4 * i + 1]), __float_as_uint(acc[c + 4 * i + 2]),
+                              __float_as_uint(acc[c + 4 * i + 3])));
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 32; r += 4) {
+            const int row = r + (lane >> 3), unit = lane & 7;
+            put(row, c + unit * 4, lds_float4(buffer + row * 128 + ((unit ^ (row & 7)) << 4)));
         }
+    }
 }
 
 // The grid's work.  Tiles go to the CTA pairs in order (columns fastest); the
@@ -625,14 +646,12 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                 if (lane == 0)
                     cluster_arrive(empty0 + b * 8);
             }
-            const int64_t m = m0 + static_cast<int64_t>(rank) * 128 + quarter * 32 + lane;
-            const int64_t nbase = n0 + half * 128;
+            const int row0 = static_cast<int>(rank) * 128 + quarter * 32;
+            const uint32_t buffer = raw + kStages * kRawBytes + (warp - 4 - 2 * kTeam) * kTurnBytes;
             if (part >= 0) {
-                float *to = a.parts + (part * kPairM + rank * 128 + quarter * 32 + lane) * kPairN + half * 128;
+                float *to = a.parts + (part * kPairM + row0) * kPairN + half * 128;
                 if (ok)
-#pragma unroll
-                    for (int i = 0; i < 128; i += 4)
-                        *reinterpret_cast<float4 *>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                    write_turned(acc, buffer, [&](int row, int col, float4 v) { *reinterpret_cast<float4 *>(to + row * kPairN + col) = v; });
                 continue;
             }
             // scale and shift of the tile's 256 columns as binary32 in shared memory
@@ -641,14 +660,23 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             affine[c] = a.scale && n0 + c < a.hidden ? load_param(a.scale, a.param_dtype, n0 + c) : 1.f;
             affine[256 + c] = a.shift && n0 + c < a.hidden ? load_param(a.shift, a.param_dtype, n0 + c) : 0.f;
             named_barrier_sync(1, 256);
-            if (!ok || m >= a.out)
+            if (!ok)
                 continue;
-            const float sum = a.shift ? a.dy_sum[m] : 0.f;
-            if (a.dtype == kTypeF32)
-                finish_row(acc, affine + half * 128, sum, static_cast<float *>(a.dw) + m * a.hidden + nbase, a.hidden - nbase, a.accumulate);
-            else
-                finish_row(acc, affine + half * 128, sum, static_cast<__nv_bfloat16 *>(a.dw) + m * a.hidden + nbase, a.hidden - nbase,
-                           a.accumulate);
+            const int64_t mbase = static_cast<int64_t>(m0) + row0, nbase = n0 + half * 128;
+            const float own_sum = a.shift && mbase + lane < a.out ? a.dy_sum[mbase + lane] : 0.f;
+            write_turned(acc, buffer, [&](int row, int col, float4 v) {
+                const float sum = __shfl_sync(kFullMask, own_sum, row);
+                if (mbase + row >= a.out || nbase + col >= a.hidden)
+                    return;
+                const float4 s = *reinterpret_cast<const float4 *>(affine + half * 128 + col);
+                const float4 t = *reinterpret_cast<const float4 *>(affine + 256 + half * 128 + col);
+                v = make_float4(fmaf(sum, t.x, v.x * s.x), fmaf(sum, t.y, v.y * s.y), fmaf(sum, t.z, v.z * s.z), fmaf(sum, t.w, v.w * s.w));
+                const int64_t i = (mbase + row) * a.hidden + nbase + col;
+                if (a.dtype == kTypeF32)
+                    store4(static_cast<float *>(a.dw) + i, v, a.accumulate);
+                else
+                    store4(static_cast<__nv_bfloat16 *>(a.dw) + i, v, a.accumulate);
+            });
         }
     }
     tc_fence_before_sync();
