@@ -12,7 +12,6 @@
 #include "taco.h"
 #include "taco_host.h"
 #include "taco_kernels.h"
-#include "taco_train.h"
 
 namespace taco {
 namespace {
@@ -81,12 +80,6 @@ void init_device(DeviceState &st)
             for (int k = 0; k < 6 && e == cudaSuccess; k++)
                 e = init_kernel(reduce_kernel_info(blocks[i], code, reduce_shards[k]), &st.ctas_per_sm);
     }
-    if (e == cudaSuccess)
-        e = init_weight_grad();
-    if (e == cudaSuccess)
-        e = init_norm();
-    if (e == cudaSuccess)
-        e = init_norm_grad();
     st.init_error = e;
 }
 

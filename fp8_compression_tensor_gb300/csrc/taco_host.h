@@ -19,6 +19,8 @@ struct DeviceState {
     int sm_count = 0;
     uint32_t *fault = nullptr;  // device address of the fault flags
     int ctas_per_sm = 0;        // last occupancy query (set-up check only)
+    std::once_flag train_once;  // set-up of the training operators' kernels
+    cudaError_t train_error = cudaSuccess;
 };
 
 // Set-up of the current device, once per device and process.

@@ -410,9 +410,10 @@ cudaError_t norm_vectors(const NormArgs &a, int sms, cudaStream_t stream)
     int groups = row_groups(a.rows, warps, kNormThreads, sms);
     const int threads = warps * groups * 32;
     const int64_t ctas = (a.rows + groups - 1) / groups;
-    const bool staged = ctas > sms && (a.weight || a.bias);
-    const size_t params = staged ? 8 * static_cast<size_t>(a.hidden) : 0;
     const size_t stage = static_cast<size_t>(a.residual ? 2 : 1) * nv * threads * 8 * sizeof(T);
+    // (the widest binary32 rows with a residual leave no room for the parameters)
+    const bool staged = ctas > sms && (a.weight || a.bias) && 8 * static_cast<size_t>(a.hidden) + stage <= kMaxShared;
+    const size_t params = staged ? 8 * static_cast<size_t>(a.hidden) : 0;
     int stages = ring_stages(params, stage);
     void *p[] = {&args, &warps, &groups, &stages};
     return launch_kernel(norm_kernel<T>(nv, staged, a.hidden == warps * nv * 256), static_cast<int>(std::min<int64_t>(ctas, sms)), threads,

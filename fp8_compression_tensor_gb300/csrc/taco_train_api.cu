@@ -64,6 +64,24 @@ int column_parts(int64_t rows)
     return static_cast<int>(rows < kMaxColumnParts ? rows : kMaxColumnParts);
 }
 
+// Set-up of the current device and, once, of these operators' kernels.
+taco_status_t training_device(DeviceState **out)
+{
+    const taco_status_t st = device_state(out);
+    if (st != TACO_OK)
+        return st;
+    DeviceState *dev = *out;
+    std::call_once(dev->train_once, [dev] {
+        cudaError_t e = init_weight_grad();
+        if (e == cudaSuccess)
+            e = init_norm();
+        if (e == cudaSuccess)
+            e = init_norm_grad();
+        dev->train_error = e;
+    });
+    return dev->train_error == cudaSuccess ? TACO_OK : cuda_fail(dev->train_error);
+}
+
 taco_status_t done(cudaError_t e) { return e == cudaSuccess ? TACO_OK : cuda_fail(e); }
 
 }  // namespace
@@ -93,7 +111,7 @@ taco_status_t taco_layernorm(const taco_layernorm_args_t *a, taco_stream_t strea
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = device_state(&dev)) != TACO_OK)
+    if ((st = training_device(&dev)) != TACO_OK)
         return st;
     const NormArgs k{a->x,    a->residual, a->weight, a->bias,   a->y,   a->summed,      a->mean,  a->rstd,
                      static_cast<uint8_t *>(a->packed), a->rows, a->hidden, a->eps, a->param_dtype, a->block, a->code};
@@ -146,7 +164,7 @@ taco_status_t taco_layernorm_backward(const taco_layernorm_backward_args_t *a, t
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = device_state(&dev)) != TACO_OK)
+    if ((st = training_device(&dev)) != TACO_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     float *ws = sums ? static_cast<float *>(a->workspace) : nullptr;
@@ -180,7 +198,7 @@ taco_status_t taco_gelu(const taco_gelu_args_t *a, taco_stream_t stream)
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = device_state(&dev)) != TACO_OK)
+    if ((st = training_device(&dev)) != TACO_OK)
         return st;
     const GeluArgs k{a->x, a->bias, a->y, static_cast<uint8_t *>(a->packed), a->rows, a->hidden,
                      a->param_dtype, a->tanh_form, a->block, a->code};
@@ -224,7 +242,7 @@ taco_status_t taco_gelu_backward(const taco_gelu_backward_args_t *a, taco_stream
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = device_state(&dev)) != TACO_OK)
+    if ((st = training_device(&dev)) != TACO_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     float *ws = a->dbias ? static_cast<float *>(a->workspace) : nullptr;
@@ -280,7 +298,7 @@ taco_status_t taco_weight_grad(const taco_weight_grad_args_t *a, taco_stream_t s
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = device_state(&dev)) != TACO_OK)
+    if ((st = training_device(&dev)) != TACO_OK)
         return st;
     const WeightGradArgs k{a->dy, static_cast<const uint8_t *>(a->packed), a->dweight, a->scale, a->shift, a->dy_sum,
                            static_cast<float *>(a->workspace), a->rows, a->out, a->hidden, a->dtype, a->param_dtype,

@@ -71,6 +71,18 @@ def test_norm(taco, rows, hidden, dtype, pdtype):
     check_norm(taco, rows, hidden, dtype, pdtype, residual=True)
 
 
+@pytest.mark.parametrize("dtype", (BF16, F32))
+@pytest.mark.parametrize("hidden", (12288, 16376, 16384, 16383))
+def test_norm_wide_rows_on_every_sm(taco, dtype, hidden):
+    """More rows than SMs at the widest rows that registers hold: shared memory
+    is full of rows and parameters."""
+    block = 128 if hidden % 128 == 0 else None
+    check_norm(taco, 170, hidden, dtype, F32, residual=True, block=block)
+    check_norm(taco, 170, hidden, dtype, F32)
+    check_norm_grad(taco, 170, hidden, dtype, F32, dsummed=True)
+    check_norm_grad(taco, 170, hidden, dtype, F32, dsummed=True, block=block)
+
+
 @pytest.mark.parametrize("affine,pdtype", [(False, F32), (True, BF16), (True, F16)])
 def test_norm_parameters(taco, affine, pdtype):
     for hidden in (33, 1024, 4096):
