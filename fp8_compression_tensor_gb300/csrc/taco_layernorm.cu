@@ -13,7 +13,7 @@ namespace taco {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Any width: one CTA per row, element by element
+// Odd widths too large for shared memory: one CTA per row, element by element
 // ---------------------------------------------------------------------------
 
 template <typename T>
@@ -56,29 +56,112 @@ __global__ void __launch_bounds__(kRowThreads) taco_norm_any_kernel(NormArgs a)
                 v += load_param(a.bias, a.param_dtype, c);
             static_cast<T *>(a.y)[row * C + c] = from_float<T>(v);
         }
-        if (!a.packed)
-            continue;
-        // Records: a warp per block.
-        const int lane = threadIdx.x & 31, B = a.block;
-        for (int64_t k = threadIdx.x >> 5; k < C / B; k += kRowThreads / 32) {
-            uint32_t top = 0;
-            for (int i = lane; i < B; i += 32)
-                top = max(top, abs_bits((h(k * B + i) - mean) * rstd));
-            top = __reduce_max_sync(kFullMask, top);
-            float inv;
-            const float s = record_scale(top, a.code, &inv);
-            uint8_t *rec = a.packed + (row * (C / B) + k) * (B + 8);
-            for (int i = lane; i < B; i += 32)
-                rec[i] = record_code((h(k * B + i) - mean) * rstd, inv, a.code);
-            if (lane == 0)
-                *reinterpret_cast<float2 *>(rec + B) = make_float2(1.f, s);
-        }
     }
 }
 
 // ---------------------------------------------------------------------------
 // Widths of whole vectors of eight: rows in registers
 // ---------------------------------------------------------------------------
+
+// Rows of whole vectors that are too wide for registers: a CTA a row, two
+// vectors a lane at a time, the row read three times (from L1 and L2 after the
+// first).
+constexpr int kWideThreads = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) taco_norm_wide_kernel(NormArgs a)
+{
+    __shared__ float part[32];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t C = a.hidden;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *x = static_cast<const T *>(a.x) + row * C;
+        const T *res = a.residual ? static_cast<const T *>(a.residual) + row * C : nullptr;
+        auto load = [&](int64_t c, bool store) {
+            F8 h = unpack(load_raw8(x + c));
+            if (res) {
+                const F8 r = unpack(load_raw8(res + c));
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    h.v[i] = add2(h.v[i], r.v[i]);
+                const Raw8<T> o = pack<T>(h);
+                if (store)
+                    store_raw8(static_cast<T *>(a.summed) + row * C + c, o);
+                h = unpack(o);
+            }
+            return h;
+        };
+        // f(c, j) for the lane's vectors; j numbers the two of a step
+        auto each = [&](auto f) {
+            for (int64_t base = warp * 512; base < C; base += kWideThreads * 16)
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    if (base + j * 256 + lane * 8 < C)
+                        f(base + j * 256 + lane * 8);
+        };
+        float2 total = both(0.f);
+        each([&](int64_t c) {
+            const F8 h = load(c, true);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                total = add2(total, h.v[i]);
+        });
+        const float mean = cta_sum(total.x + total.y, part) / static_cast<float>(C);
+        float2 squares = both(0.f);
+        each([&](int64_t c) {
+            const F8 h = load(c, false);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 v = add2(h.v[i], both(-mean));
+                squares = fma2(v, v, squares);
+            }
+        });
+        const float rstd = inv_sqrt(cta_sum(squares.x + squares.y, part) / static_cast<float>(C) + a.eps);
+        if (threadIdx.x == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        for (int64_t base = warp * 512; base < C; base += kWideThreads * 16) {
+            F8 h[2];
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int64_t c = base + j * 256 + lane * 8;
+                if (c < C) {
+                    h[j] = load(c, false);
+                    F8 y;
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        y.v[i] = h[j].v[i] = mul2(add2(h[j].v[i], both(-mean)), both(rstd));
+                    if (a.weight) {
+                        const F8 w = load_param_f8(a.weight, a.param_dtype, c);
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            y.v[i] = mul2(y.v[i], w.v[i]);
+                    }
+                    if (a.bias) {
+                        const F8 b = load_param_f8(a.bias, a.param_dtype, c);
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            y.v[i] = add2(y.v[i], b.v[i]);
+                    }
+                    store_raw8(static_cast<T *>(a.y) + row * C + c, pack<T>(y));
+                }
+            }
+            if (a.packed) {
+                const int left = static_cast<int>(C - base < 512 ? C - base : 512), col[2] = {lane * 8, 256 + lane * 8};
+                uint8_t *to = a.packed + (row * C + base) / a.block * (a.block + 8);
+                if (a.code == 0)
+                    write_records<2, 0>(h, col, left, to, a.block);
+                else if (a.code == 1)
+                    write_records<2, 1>(h, col, left, to, a.block);
+                else
+                    write_records<2, 2>(h, col, left, to, a.block);
+            }
+        }
+    }
+}
 
 // A row's columns over a group of `warps` warps: vector j (of NV) of warp w
 // starts at column 256 (w NV + j), lane l holds eight columns from 8 l on.  The
@@ -426,8 +509,13 @@ cudaError_t norm_any(const NormArgs &a, int sms, cudaStream_t stream)
     cudaError_t result;
     if (fits_registers(a.hidden) && a.hidden % 8 == 0)
         return norm_vectors<T>(a, sms, stream);
-    if (fits_registers(a.hidden) && norm_odd<T>(a, sms, stream, &result))
+    if (fits_registers(a.hidden) && a.hidden % 8 && norm_odd<T>(a, sms, stream, &result))
         return result;
+    if (a.hidden % 8 == 0) {
+        NormArgs args = a;
+        void *p[] = {&args};
+        return launch_kernel(reinterpret_cast<void *>(&taco_norm_wide_kernel<T>), row_grid(a.rows, sms, 4), kWideThreads, 0, stream, p);
+    }
     NormArgs args = a;
     void *p[] = {&args};
     return launch_kernel(reinterpret_cast<void *>(&taco_norm_any_kernel<T>), row_grid(a.rows, sms, 8), kRowThreads, 0,

@@ -10,7 +10,7 @@ namespace taco {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Any width: one CTA per row, element by element
+// Odd widths too large for shared memory: one CTA per row, element by element
 // ---------------------------------------------------------------------------
 
 // dx of any width: one CTA per row.
@@ -23,10 +23,9 @@ __global__ void __launch_bounds__(kRowThreads) taco_norm_grad_any_kernel(NormGra
     const int64_t C = a.hidden;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *dy = static_cast<const T *>(a.dy) + row * C;
-        const float rstd = a.rstd[row], mean = a.x ? a.mean[row] : 0.f;
+        const float rstd = a.rstd[row], mean = a.mean[row];
         auto xhat = [&](int64_t c) {
-            return a.x ? (to_float(static_cast<const T *>(a.x)[row * C + c]) - mean) * rstd
-                       : record_value(a.packed, row * C + c, a.block, a.code);
+            return (to_float(static_cast<const T *>(a.x)[row * C + c]) - mean) * rstd;
         };
         auto grad = [&](int64_t c) {
             const float v = to_float(dy[c]);
@@ -61,8 +60,7 @@ __global__ void __launch_bounds__(128) taco_norm_grad_columns_kernel(NormGradArg
     float dw = 0.f, db = 0.f;
     for (int64_t row = blockIdx.y; row < a.rows; row += a.nparts) {
         const float g = to_float(static_cast<const T *>(a.dy)[row * C + c]);
-        const float xh = a.x ? (to_float(static_cast<const T *>(a.x)[row * C + c]) - a.mean[row]) * a.rstd[row]
-                             : record_value(a.packed, row * C + c, a.block, a.code);
+        const float xh = (to_float(static_cast<const T *>(a.x)[row * C + c]) - a.mean[row]) * a.rstd[row];
         dw = fmaf(g, xh, dw);
         db += g;
     }
@@ -73,6 +71,105 @@ __global__ void __launch_bounds__(128) taco_norm_grad_columns_kernel(NormGradArg
 // ---------------------------------------------------------------------------
 // Widths of whole vectors of eight
 // ---------------------------------------------------------------------------
+
+// xhat of eight columns from c on.
+template <typename T>
+__device__ __forceinline__ F8 load_normalised(const NormGradArgs &a, int64_t row, int64_t c, float mean, float rstd)
+{
+    F8 f;
+    if (a.x) {
+        f = unpack(load_raw8(static_cast<const T *>(a.x) + row * a.hidden + c));
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            f.v[i] = mul2(add2(f.v[i], both(-mean)), both(rstd));
+    } else {
+        const int64_t k = (row * a.hidden + c) / a.block;
+        const uint8_t *rec = a.packed + k * (a.block + 8);
+        f = codes8_to_float(__ldg(reinterpret_cast<const uint2 *>(rec + (row * a.hidden + c - k * a.block))), a.code);
+        const float s = record_s(rec, a.block);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            f.v[i] = mul2(f.v[i], both(s));
+    }
+    return f;
+}
+
+// Rows too wide for registers and shared memory: dx with a CTA a row, read twice,
+// and the column sums in a pass of their own.
+constexpr int kWideThreads = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) taco_norm_grad_wide_kernel(NormGradArgs a)
+{
+    __shared__ float part[32];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t C = a.hidden;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float rstd = a.rstd[row], mean = a.x ? a.mean[row] : 0.f;
+        auto weighted = [&](int64_t c) {
+            F8 g = unpack(load_raw8(static_cast<const T *>(a.dy) + row * C + c));
+            if (a.weight) {
+                const F8 w = load_param_f8(a.weight, a.param_dtype, c);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    g.v[i] = mul2(g.v[i], w.v[i]);
+            }
+            return g;
+        };
+        float2 t1 = both(0.f), t2 = both(0.f);
+        for (int64_t c = threadIdx.x * 8; c < C; c += kWideThreads * 8) {
+            const F8 w = weighted(c), xh = load_normalised<T>(a, row, c, mean, rstd);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                t1 = add2(t1, w.v[i]);
+                t2 = fma2(w.v[i], xh.v[i], t2);
+            }
+        }
+        const float c1 = cta_sum(t1.x + t1.y, part) / static_cast<float>(C), c2 = cta_sum(t2.x + t2.y, part) / static_cast<float>(C);
+        for (int64_t c = threadIdx.x * 8; c < C; c += kWideThreads * 8) {
+            F8 w = weighted(c);
+            const F8 xh = load_normalised<T>(a, row, c, mean, rstd);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                w.v[i] = mul2(fma2(xh.v[i], both(-c2), add2(w.v[i], both(-c1))), both(rstd));
+            if (a.dsummed) {
+                const F8 s = unpack(load_raw8(static_cast<const T *>(a.dsummed) + row * C + c));
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    w.v[i] = add2(w.v[i], s.v[i]);
+            }
+            store_raw8(static_cast<T *>(a.dx) + row * C + c, pack<T>(w));
+        }
+    }
+}
+
+// Column sums over the rows part, part + nparts, ...: eight columns a thread.
+template <typename T>
+__global__ void __launch_bounds__(128) taco_norm_grad_wide_columns_kernel(NormGradArgs a)
+{
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t C = a.hidden, c = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) * 8;
+    if (c >= C)
+        return;
+    F8 dw, db;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        dw.v[i] = db.v[i] = both(0.f);
+#pragma unroll 4
+    for (int64_t row = blockIdx.y; row < a.rows; row += a.nparts) {
+        const F8 g = unpack(load_raw8(static_cast<const T *>(a.dy) + row * C + c));
+        const F8 xh = load_normalised<T>(a, row, c, a.x ? a.mean[row] : 0.f, a.rstd[row]);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            dw.v[i] = fma2(g.v[i], xh.v[i], dw.v[i]);
+            db.v[i] = add2(db.v[i], g.v[i]);
+        }
+    }
+    store_raw8(a.parts + static_cast<int64_t>(blockIdx.y) * C + c, pack<float>(dw));
+    store_raw8(a.parts + static_cast<int64_t>(a.nparts + blockIdx.y) * C + c, pack<float>(db));
+}
 
 // The forward pass's layout, so a thread keeps its columns and adds up their
 // dweight and dbias in registers over all rows that its group takes.  The
@@ -529,6 +626,18 @@ cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
             void *p[] = {a, &warps, &groups, &stages};
             return launch_kernel(norm_grad_kernel<T>(nv, records ? a->code : -1, C == warps * nv * 256), a->nparts, threads, smem, stream, p);
         }
+    }
+    if (C % 8 == 0) {
+        // about eight CTAs of 128 threads an SM
+        const int64_t across = (C + 1023) / 1024;
+        a->nparts = static_cast<int>(std::min<int64_t>({a->rows, kMaxColumnParts, std::max<int64_t>(1, 8 * sms / across)}));
+        void *p[] = {a};
+        cudaError_t e = launch_kernel(reinterpret_cast<void *>(&taco_norm_grad_wide_kernel<T>), row_grid(a->rows, sms, 4), kWideThreads, 0,
+                                      stream, p);
+        if (e == cudaSuccess && a->parts)
+            e = launch_kernel_2d(reinterpret_cast<void *>(&taco_norm_grad_wide_columns_kernel<T>), static_cast<unsigned>(across),
+                                 static_cast<unsigned>(a->nparts), 128, 0, stream, p);
+        return e;
     }
     void *p[] = {a};
     cudaError_t e = launch_kernel(reinterpret_cast<void *>(&taco_norm_grad_any_kernel<T>), row_grid(a->rows, sms, 8),

@@ -215,25 +215,6 @@ __device__ __forceinline__ float record_scale(uint32_t max_bits, int code, float
     return ordinary ? __int_as_float(bits) : max_bits == 0u ? 0.f : __uint_as_float(0x7fc00000u);
 }
 
-// Code byte of u / s (|u / s| <= Q_max; the product with the power of two 1/s is exact
-// or, for a subnormal u, exact as well).
-__device__ __forceinline__ uint8_t record_code(float u, float inv, int code)
-{
-    const float v = inv == 0.f ? 0.f : __fmul_rn(u, inv);
-    return static_cast<uint8_t>(encode4(code, v, 0.f, 0.f, 0.f) & 0xffu);
-}
-
-// The two values of the two code bytes in the low 16 bits of `pair`.
-__device__ __forceinline__ float2 codes2_to_float2(uint32_t pair, int code)
-{
-    if (code == 0)
-        return e4m3x2_to_float2(pair);
-    if (code == 1)
-        return e5m2x2_to_float2(pair);
-    return make_float2(static_cast<float>(static_cast<int8_t>(pair & 0xffu)),
-                       static_cast<float>(static_cast<int8_t>((pair >> 8) & 0xffu)));
-}
-
 // Eight code bytes as floats.
 __device__ __forceinline__ F8 codes8_to_float(uint2 c, int code)
 {
@@ -313,21 +294,6 @@ __device__ __forceinline__ void write_records(const F8 (&u)[NV], const int (&col
     for (int j = 0; j < NV; j++)
         if (col[j] < C)
             write_codes<CODE>(u[j], top[j], row + col[j] + (col[j] >> shift) * 8, col[j] & (block - 1), block);
-}
-
-// Byte of element `col` in a record row.
-__device__ __forceinline__ int64_t record_offset(int64_t col, int block)
-{
-    const int64_t k = col / block;
-    return k * (block + 8) + (col - k * block);
-}
-
-// Value of element (row, col) of packed records of [rows, hidden].
-__device__ __forceinline__ float record_value(const uint8_t *packed, int64_t index, int block, int code)
-{
-    const int64_t k = index / block;
-    const uint8_t *rec = packed + k * (block + 8);
-    return codes2_to_float2(rec[index - k * block], code).x * record_s(rec, block);
 }
 
 // ---------------------------------------------------------------------------

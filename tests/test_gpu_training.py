@@ -513,6 +513,16 @@ def test_other_stream(taco):
             assert torch.equal(a, b)
 
 
+def test_default_stream_as_a_number(taco):
+    args = inputs(40, 512)
+    want = every_call(taco, *args)
+    torch.cuda.synchronize()
+    for a, b in zip(want, every_call(taco, *args, stream=0)):
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
+    assert taco.device_status(device="cuda") == 0
+
+
 def test_graph_capture(taco):
     args = inputs()
     want = every_call(taco, *args)
