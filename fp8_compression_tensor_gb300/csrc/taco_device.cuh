@@ -39,7 +39,6 @@ constexpr float kDivFastMin = 0x1p-100f;
 constexpr uint32_t kFaultCompress = 1u;
 constexpr uint32_t kFaultDecompress = 2u;
 constexpr uint32_t kFaultReduce = 4u;
-constexpr uint32_t kFaultWeightGrad = 16u;
 constexpr uint32_t kFaultSelfTest = 8u;   // the wait-timeout self-test (taco_selftest_wait_timeout)
 
 // A wait on the copy engine gives up after this long (nanoseconds).

@@ -23,11 +23,10 @@ struct KernelInfo {
 // Launches `fn` with programmatic stream serialisation (when TACO_PDL): the
 // kernel may be scheduled while the previous kernel in the stream finishes;
 // the kernels order their memory accesses with griddepcontrol.wait.
-inline cudaError_t launch_kernel_2d(const void *fn, unsigned grid_x, unsigned grid_y, int threads, size_t smem,
-                                    cudaStream_t stream, void **args)
+inline cudaError_t launch_kernel(const void *fn, int grid, int threads, size_t smem, cudaStream_t stream, void **args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid_x, grid_y);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -37,11 +36,6 @@ inline cudaError_t launch_kernel_2d(const void *fn, unsigned grid_x, unsigned gr
     cfg.attrs = attr;
     cfg.numAttrs = TACO_PDL ? 1 : 0;
     return cudaLaunchKernelExC(&cfg, fn, args);
-}
-
-inline cudaError_t launch_kernel(const void *fn, int grid, int threads, size_t smem, cudaStream_t stream, void **args)
-{
-    return launch_kernel_2d(fn, static_cast<unsigned>(grid), 1u, threads, smem, stream, args);
 }
 
 // Compression scheme: the method (ASH + DS with E4M3 codes) or one of the

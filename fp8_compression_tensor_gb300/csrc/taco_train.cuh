@@ -22,6 +22,9 @@
 
 namespace taco {
 
+// Fault flag of the weight gradient, next to those of the codec (taco_device.cuh).
+constexpr uint32_t kFaultWeightGrad = 16u;
+
 // ---------------------------------------------------------------------------
 // Typed elements
 // ---------------------------------------------------------------------------

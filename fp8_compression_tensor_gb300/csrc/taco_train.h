@@ -6,12 +6,31 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "taco_kernels.h"
+
 namespace taco {
 
 // Element types (taco_dtype_t).
 constexpr int kTypeBf16 = 0;
 constexpr int kTypeF16 = 1;
 constexpr int kTypeF32 = 2;
+
+// launch_kernel (taco_kernels.h) with a two-dimensional grid.
+inline cudaError_t launch_kernel_2d(const void *fn, unsigned grid_x, unsigned grid_y, int threads, size_t smem,
+                                    cudaStream_t stream, void **args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid_x, grid_y);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = TACO_PDL ? 1 : 0;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
 
 // Most row chunks whose column sums a backward pass keeps apart (two CTAs on each of 152 SMs).
 constexpr int kMaxColumnParts = 304;
