@@ -491,13 +491,16 @@ cudaError_t norm_vectors(const NormArgs &a, int sms, cudaStream_t stream)
     const int nv = lane_vectors(a.hidden);
     int warps = static_cast<int>((a.hidden + 256 * nv - 1) / (256 * nv));
     int groups = row_groups(a.rows, warps, kNormThreads, sms);
+    const size_t place = static_cast<size_t>(a.residual ? 2 : 1) * nv * warps * 256 * sizeof(T);
+    while (groups > 1 && 8 * static_cast<size_t>(a.hidden) + groups * place > max_shared<T>(196))
+        groups--;
     const int threads = warps * groups * 32;
     const int64_t ctas = (a.rows + groups - 1) / groups;
-    const size_t stage = static_cast<size_t>(a.residual ? 2 : 1) * nv * threads * 8 * sizeof(T);
+    const size_t stage = groups * place;
     // (the widest binary32 rows with a residual leave no room for the parameters)
     const bool staged = ctas > sms && (a.weight || a.bias) && 8 * static_cast<size_t>(a.hidden) + stage <= kMaxShared;
     const size_t params = staged ? 8 * static_cast<size_t>(a.hidden) : 0;
-    int stages = ring_stages(params, stage);
+    int stages = ring_stages(params, stage, max_shared<T>(196));
     void *p[] = {&args, &warps, &groups, &stages};
     return launch_kernel(norm_kernel<T>(nv, staged, a.hidden == warps * nv * 256), static_cast<int>(std::min<int64_t>(ctas, sms)), threads,
                          params + stages * stage, stream, p);

@@ -614,11 +614,12 @@ cudaError_t norm_grad_any(NormGradArgs *a, int sms, cudaStream_t stream)
         const size_t weight = static_cast<size_t>(4 * C);
         const size_t place = static_cast<size_t>(1 + !records + (a->dsummed != nullptr)) * nv * warps * 256 * sizeof(T) +
                              (records ? (C / a->block * (a->block + 8) + 8 + 15) / 16 * 16 : 0);
-        while (records && groups > 1 && ring_stages(weight, groups * place) < 3)   // fewer groups, to fit three rows of each
+        // fewer groups where their rows do not fit, with records three of each
+        while (groups > 1 && (weight + groups * place > max_shared<T>(180) || (records && ring_stages(weight, groups * place) < 3)))
             groups--;
         const int threads = warps * groups * 32;
         const size_t stage = groups * place;
-        int stages = ring_stages(weight, stage);
+        int stages = std::max(ring_stages(weight, stage, max_shared<T>(180)), records ? std::min(ring_stages(weight, stage), 3) : 1);
         const size_t smem = weight + std::max<size_t>(stages * stage, groups > 1 ? 8 * static_cast<size_t>(C) * groups : 0);
         if (smem <= kMaxShared && (!records || stages >= 3)) {
             a->nparts = static_cast<int>(std::min({(a->rows + groups - 1) / groups, static_cast<int64_t>(sms),

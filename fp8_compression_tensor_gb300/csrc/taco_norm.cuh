@@ -42,8 +42,9 @@ constexpr int kNormThreads = 768, kGradThreads = 512;   // the backward pass kee
 // will read itself, so these need no barrier, only the thread's own wait.
 // A lane's eight binary32 values are two copies of 16 bytes, each of half a
 // 32-byte sector, so these go through L1 (.ca) and the second one finds the
-// sector there: 8192 x 4096 forward with a residual 123 -> 105 us, backward 142
-// -> 121.  Rows of 16-bit elements pass it by (.cg): through it, 26 -> 33 us.
+// sector there: 8192 x 4096 with a residual takes 84 us forward and 94 backward,
+// past L1 it took 123 and 142.  Rows of 16-bit elements pass it by (.cg): through
+// it, 26 -> 33 us.
 template <typename T>
 __device__ __forceinline__ void copy16(uint32_t to, const void *from)
 {
@@ -138,12 +139,24 @@ int row_groups(int64_t rows, int warps, int threads, int sms)
     return static_cast<int>(std::min(fit, spread));
 }
 
-// Rows in flight: up to four in the shared memory that the parameters leave.
-int ring_stages(size_t params, size_t stage, int most = 4)
+// Shared memory for the rows of a type.  Binary32 rows are copied through L1,
+// which has what shared memory leaves of 256 KB: with about 60 KB (forward) and
+// 76 KB (backward) of it the copies' second halves are still there.  8192 x 4096
+// with a residual takes 84 us forward, 104 at 228 KB of shared memory; backward 94
+// against 120 at 213 KB.
+template <typename T>
+constexpr size_t max_shared(int kb)
 {
-    while (most > 1 && params + most * stage > kMaxShared)
-        most--;
-    return most;
+    return sizeof(T) == 4 ? static_cast<size_t>(kb) * 1024 : kMaxShared;
+}
+
+// Rows in flight: up to four in the shared memory that the parameters leave.
+int ring_stages(size_t params, size_t stage, size_t limit = kMaxShared)
+{
+    int stages = 4;
+    while (stages > 1 && params + stages * stage > limit)
+        stages--;
+    return stages;
 }
 
 }  // namespace
