@@ -16,6 +16,7 @@ Argument marshalling only, like _binding.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import struct
 from typing import NamedTuple, Optional
@@ -92,6 +93,17 @@ def _library() -> ctypes.CDLL:
     return _lib
 
 
+@functools.lru_cache(maxsize=512)
+def _record_bytes(rows: int, hidden: int, block: int) -> int:
+    return compressed_bytes(rows, hidden, block)
+
+
+@functools.lru_cache(maxsize=512)
+def _workspace_bytes(query: str, *sizes: int) -> int:
+    """The library's answer for these sizes; 0 for sizes that the call itself refuses."""
+    return max(getattr(_library(), query)(*sizes), 0)
+
+
 class LayerNorm(NamedTuple):
     y: torch.Tensor
     mean: torch.Tensor
@@ -164,7 +176,7 @@ def _param_type(t, name: str):
 
 
 def _packed(packed, rows: int, hidden: int, block: int, device: int) -> int:
-    return _tensor(packed, "packed", device, torch.uint8, (compressed_bytes(rows, hidden, block),))
+    return _tensor(packed, "packed", device, torch.uint8, (_record_bytes(rows, hidden, block),))
 
 
 def _run(device: int, stream, call):
@@ -200,7 +212,7 @@ def layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opti
     pr = _tensor(residual, "residual", device, x.dtype, shape)
     pw = _tensor(weight, "weight", device, pdtype, width)
     pb = _tensor(bias, "bias", device, pdtype, width)
-    nbytes = compressed_bytes(rows, hidden, block) if checkpoint else 0
+    nbytes = _record_bytes(rows, hidden, block) if checkpoint else 0
 
     def call(handle):
         y = torch.empty_like(x)
@@ -248,7 +260,7 @@ def layernorm_backward(dy: torch.Tensor, rstd: torch.Tensor, weight: Optional[to
         if weight is not None:
             dweight = torch.empty_like(weight)
             dbias = torch.empty_like(weight) if bias_grad else None
-            nbytes = lib.taco_layernorm_backward_workspace(rows, hidden)
+            nbytes = _workspace_bytes("taco_layernorm_backward_workspace", rows, hidden)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
         rc = lib.taco_layernorm_backward(
             _pack_layernorm_backward(dy.data_ptr(), px, pmean, prstd, ppacked, pw, pds, dx.data_ptr(), _address(dweight),
@@ -276,7 +288,7 @@ def gelu(x: torch.Tensor, bias: Optional[torch.Tensor] = None, approximate: str 
     device = x.get_device()
     pdtype = _param_type(bias, "bias")
     pb = _tensor(bias, "bias", device, pdtype, (hidden,))
-    nbytes = compressed_bytes(rows, hidden, block) if checkpoint else 0
+    nbytes = _record_bytes(rows, hidden, block) if checkpoint else 0
 
     def call(handle):
         y = torch.empty_like(x)
@@ -312,7 +324,7 @@ def gelu_backward(dy: torch.Tensor, packed: torch.Tensor, approximate: str = "no
         nbytes = 0
         if bias_dtype is not None:
             dbias = torch.empty(hidden, dtype=bias_dtype, device=dy.device)
-            nbytes = lib.taco_gelu_backward_workspace(rows, hidden)
+            nbytes = _workspace_bytes("taco_gelu_backward_workspace", rows, hidden)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
         rc = lib.taco_gelu_backward(
             _pack_gelu_backward(dy.data_ptr(), ppacked, dx.data_ptr(), _address(y), _address(dbias), _address(ws), nbytes, rows,
@@ -358,7 +370,7 @@ def weight_grad(dy: torch.Tensor, packed: torch.Tensor, hidden: int, block: int 
 
     def call(handle):
         dw = torch.empty((features, hidden), dtype=dtype, device=dy.device) if out is None else out
-        nbytes = max(lib.taco_weight_grad_workspace(rows, features, hidden), 0)
+        nbytes = _workspace_bytes("taco_weight_grad_workspace", rows, features, hidden)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
         rc = lib.taco_weight_grad(
             _pack_weight_grad(dy.data_ptr(), ppacked, dw.data_ptr(), pscale, pshift, psum, _address(ws), nbytes, rows, features,
