@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGra
     auto fetch = [&](int64_t row) {
         if (in && row < a.rows) {
             next_dy = load_raw8(static_cast<const T *>(a.dy) + row * C + col);
-            next_codes = __ldg(reinterpret_cast<const uint2 *>(rec + row * pitch + within));
-            next_s = __ldg(reinterpret_cast<const float *>(rec + row * pitch + a.block + 4));
+            next_codes = *reinterpret_cast<const uint2 *>(rec + row * pitch + within);
+            next_s = *reinterpret_cast<const float *>(rec + row * pitch + a.block + 4);
         }
     };
     int64_t row = static_cast<int64_t>(blockIdx.y) * rows_a_pass + mine;

@@ -85,7 +85,7 @@ __device__ __forceinline__ F8 load_normalised(const NormGradArgs &a, int64_t row
     } else {
         const int64_t k = (row * a.hidden + c) / a.block;
         const uint8_t *rec = a.packed + k * (a.block + 8);
-        f = codes8_to_float(__ldg(reinterpret_cast<const uint2 *>(rec + (row * a.hidden + c - k * a.block))), a.code);
+        f = codes8_to_float(*reinterpret_cast<const uint2 *>(rec + (row * a.hidden + c - k * a.block)), a.code);
         const float s = record_s(rec, a.block);
 #pragma unroll
         for (int i = 0; i < 4; i++)
@@ -237,9 +237,9 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
     float next_rstd = 0.f, next_mean = 0.f;
     auto fetch = [&](int64_t row) {
         if (row < a.rows) {
-            next_rstd = __ldg(a.rstd + row);
+            next_rstd = a.rstd[row];
             if (!RECORDS)
-                next_mean = __ldg(a.mean + row);
+                next_mean = a.mean[row];
         }
     };
     for (int i = 0; i < stages - 1; i++)
@@ -435,8 +435,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) taco_norm_grad_odd_kernel(Nor
     float next_rstd = 0.f, next_mean = 0.f;
     auto fetch = [&](int64_t row) {
         if (row < a.rows) {
-            next_rstd = __ldg(a.rstd + row);
-            next_mean = __ldg(a.mean + row);
+            next_rstd = a.rstd[row];
+            next_mean = a.mean[row];
         }
     };
     for (int i = 0; i < stages - 1; i++)

@@ -54,7 +54,7 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T *p)
     Raw8<T> r;
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T) / 2); i++)
-        r.v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        r.v[i] = reinterpret_cast<const uint4 *>(p)[i];
     return r;
 }
 

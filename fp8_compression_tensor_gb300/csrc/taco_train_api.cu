@@ -185,7 +185,7 @@ taco_status_t taco_gelu(const taco_gelu_args_t *a, taco_stream_t stream)
     int64_t n = 0;
     taco_status_t st = check_elements(a->rows, a->hidden, &n);
     if (st == TACO_OK && a->packed)
-        st = check_records(a->hidden, a->block, a->code);
+        st = a->hidden > INT32_MAX / 2 ? TACO_ERR_BAD_SHAPE : check_records(a->hidden, a->block, a->code);   // 32-bit columns
     if (st != TACO_OK || n == 0)
         return st;
     if (!a->x || !a->y)

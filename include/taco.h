@@ -262,7 +262,8 @@ TACO_API taco_status_t taco_layernorm_backward(const taco_layernorm_backward_arg
 
 /*
  * GELU of u = x + bias (binary32): y = u Phi(u), or with tanh_form
- * y = u/2 (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))), and the records of u.
+ * y = u/2 (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))), and the records of u
+ * (hidden < 2^30 then).
  */
 typedef struct taco_gelu_args {
     const void *x;              /* in:  [rows, hidden] */

@@ -74,6 +74,8 @@ def test_null_arguments(t, kind):
     ("_GeluArgs", dict(dtype=-1), OPTIONS),
     ("_GeluArgs", dict(packed=3 * A, block=33), BLOCK),
     ("_GeluArgs", dict(packed=3 * A, hidden=130), SHAPE),
+    ("_GeluArgs", dict(packed=3 * A, hidden=1 << 31), SHAPE),
+    ("_GeluArgs", dict(hidden=1 << 31, y=None), NULL),
     ("_GeluArgs", dict(y=None), NULL),
     ("_GeluArgs", dict(bias=3 * A + 2), ALIGN),
     ("_GeluArgs", dict(packed=A + 512), OVERLAP),
