@@ -142,6 +142,7 @@ struct WgBarriers {
     uint64_t raw_empty[kStages];   // and have been decoded
     uint64_t acc_full[2];         // a chunk's accumulator is complete
     uint64_t acc_empty[2];        // even CTA: both CTAs have read the accumulator
+    uint64_t drained;             // after a wait that gave up: the products issued so far are done
     uint32_t tmem;
 };
 
@@ -203,6 +204,19 @@ __device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, uint
         }
     }
     return true;
+}
+
+// Barrier of the eight epilogue warps: whether `ok` holds for all of them.
+__device__ __forceinline__ bool epilogue_agrees(bool ok)
+{
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(static_cast<uint32_t>(ok))
+        : "memory");
+    return all != 0;
 }
 
 // MN-major operand in the 128-byte swizzled layout: rows of 64 MN-elements,
@@ -401,6 +415,7 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
             mbar_init(bar(bars.acc_full[b]), 1);
             mbar_init(bar(bars.acc_empty[b]), 16); // eight epilogue warps of each CTA
         }
+        mbar_init(bar(bars.drained), 1);
         fence_mbar_init();
         prefetch_tmap(&map_dy);
     }
@@ -484,6 +499,10 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                     if (ok)
                         pair_commit(bar(bars.acc_full[b]));
                 }
+            }
+            if (!ok) {   // no product may read memory that the CTAs give up below
+                pair_commit(bar(bars.drained));
+                mbar_wait_bounded_thread(bar(bars.drained), 0, fault, kFaultWeightGrad);
             }
         } else if (warp == 2 && lane == 0) {
             // Record bytes
@@ -651,22 +670,22 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                 if (lane == 0)
                     cluster_arrive(empty0 + b * 8);
             }
+            // All warps have read the last tile's scales, and go on or give up together (they meet at barriers below).
+            ok = epilogue_agrees(ok);
+            if (!ok)
+                break;
             const int row0 = static_cast<int>(rank) * 128 + quarter * 32;
             const uint32_t buffer = raw + kStages * kRawBytes + (warp - 4 - 2 * kTeam) * kTurnBytes;
             if (part >= 0) {
                 float *to = a.parts + (part * kPairM + row0) * kPairN + half * 128;
-                if (ok)
-                    write_turned(acc, buffer, [&](int row, int col, float4 v) { *reinterpret_cast<float4 *>(to + row * kPairN + col) = v; });
+                write_turned(acc, buffer, [&](int row, int col, float4 v) { *reinterpret_cast<float4 *>(to + row * kPairN + col) = v; });
                 continue;
             }
             // scale and shift of the tile's 256 columns as binary32 in shared memory
             const int c = threadIdx.x - (4 + 2 * kTeam) * 32;
-            named_barrier_sync(1, 256);                        // the last tile's have been read
             affine[c] = a.scale && n0 + c < a.hidden ? load_param(a.scale, a.param_dtype, n0 + c) : 1.f;
             affine[256 + c] = a.shift && n0 + c < a.hidden ? load_param(a.shift, a.param_dtype, n0 + c) : 0.f;
             named_barrier_sync(1, 256);
-            if (!ok)
-                continue;
             const int64_t mbase = static_cast<int64_t>(m0) + row0, nbase = n0 + half * 128;
             const float own_sum = a.shift && mbase + lane < a.out ? a.dy_sum[mbase + lane] : 0.f;
             write_turned(acc, buffer, [&](int row, int col, float4 v) {
