@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(256, 4) taco_gelu_kernel(GeluArgs a)
     const int C = static_cast<int>(a.hidden), col_step = static_cast<int>(step % C), col_next = 256 % C;
     int col = static_cast<int>(at % C);
     const int shift = CODE >= 0 ? 31 - __clz(a.block) : 0;
+    if (lane == 0 && at < n)   // the warp's first elements on their way to L2 while the kernel before still runs
+        bulk_prefetch_l2(x + at, static_cast<uint32_t>((n - at < 512 ? n - at : 512) * sizeof(T)));
     grid_dependency_wait();
     Raw8<T> next[2];
     auto fetch = [&](int64_t i) {

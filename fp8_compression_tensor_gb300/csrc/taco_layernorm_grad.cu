@@ -206,8 +206,17 @@ taco_norm_grad_kernel(NormGradArgs a, int warps, int groups, int stages)
 #pragma unroll
     for (int j = 0; j < NV; j++)
         col[j] = ((warp * NV + j) * 32 + lane) * 8;
-    grid_dependency_wait();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group, step = static_cast<int64_t>(gridDim.x) * groups;
+    if (warp == 0 && lane < 2 && first + lane * step < a.rows) {
+        // the group's first rows on their way to L2 while the kernel before still runs
+        const int64_t at = (first + lane * step) * C;
+        bulk_prefetch_l2(static_cast<const T *>(a.dy) + at, C * static_cast<int>(sizeof(T)));
+        if (!RECORDS)
+            bulk_prefetch_l2(static_cast<const T *>(a.x) + at, C * static_cast<int>(sizeof(T)));
+        if (a.dsummed)
+            bulk_prefetch_l2(static_cast<const T *>(a.dsummed) + at, C * static_cast<int>(sizeof(T)));
+    }
+    grid_dependency_wait();
     auto copy_row = [&](int64_t row, int stage) {
         if (row < a.rows) {
             uint32_t to = ring_at + static_cast<uint32_t>(stage * stage_bytes) + threadIdx.x * 16u;
