@@ -142,7 +142,7 @@ struct WgBarriers {
     uint64_t raw_empty[kStages];   // and have been decoded
     uint64_t acc_full[2];         // a chunk's accumulator is complete
     uint64_t acc_empty[2];        // even CTA: both CTAs have read the accumulator
-    uint64_t drained;             // after a wait that gave up: the products issued so far are done
+    uint64_t drained;             // even CTA, after a wait that gave up: the products issued so far are done
     uint32_t tmem;
 };
 
@@ -248,6 +248,12 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"(static_cast<uint16_t>(3))
         : "memory");
+}
+
+// The same in this CTA alone, for a barrier that only this thread waits for.
+__device__ __forceinline__ void own_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 consecutive tensor-memory columns of this thread's lane, complete on return.
@@ -459,10 +465,16 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                     }
                 }
             }
-            // no copy may land after the CTA is gone: the last phase of every stage that was filled
+            // No copy may land, and no commit of `empty` from the even CTA arrive, after this CTA is gone: the last phase of
+            // every stage that was filled.  That the accumulator's commit was issued after those of `empty` does not order
+            // their arrivals.  Once a wait has given up, nothing that is on its way takes as long as that wait did.
+            bool arrives = true;
             for (int i = 0; i < kStages; i++)
-                if (used >> i & 1u)
-                    mbar_wait_bounded_thread(bar(bars.a_full[i]), i < s ? phase : phase ^ 1u, fault, kFaultWeightGrad);
+                if (used >> i & 1u) {
+                    const uint32_t last = i < s ? phase : phase ^ 1u;
+                    mbar_wait_bounded_thread(bar(bars.a_full[i]), last, fault, kFaultWeightGrad);
+                    arrives = arrives && mbar_wait_bounded_thread(bar(bars.empty[i]), last, fault, kFaultWeightGrad);
+                }
         } else if (warp == 1 && lane == 0 && rank == 0) {
             int s = 0;
             uint32_t phase = 0, chunk = 0;
@@ -501,7 +513,7 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                 }
             }
             if (!ok) {   // no product may read memory that the CTAs give up below
-                pair_commit(bar(bars.drained));
+                own_commit(bar(bars.drained));
                 mbar_wait_bounded_thread(bar(bars.drained), 0, fault, kFaultWeightGrad);
             }
         } else if (warp == 2 && lane == 0) {
