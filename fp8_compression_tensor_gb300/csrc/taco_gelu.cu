@@ -89,12 +89,6 @@ __device__ __forceinline__ float2 gelu_value2(float2 u)
     return fma2(make_float2(-a.x, -a.y), q, make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
 }
 
-// v for u >= 0, -v for u < 0.
-__device__ __forceinline__ float with_sign_of(float v, float u)
-{
-    return __uint_as_float(__float_as_uint(v) ^ (__float_as_uint(u) & 0x80000000u));
-}
-
 // gelu(u) and its slope.
 template <bool TANH>
 __device__ __forceinline__ void gelu_both2(float2 u, float2 &y, float2 &slope)
@@ -117,9 +111,9 @@ __device__ __forceinline__ void gelu_both2(float2 u, float2 &y, float2 &slope)
         const float2 a = make_float2(bounded_abs(u.x), bounded_abs(u.y)), minus = make_float2(-a.x, -a.y);
         const float2 q = normal_tail2(a, e);
         const float2 r = fma2(mul2(minus, both(kInvSqrt2Pi)), e, q);
-        // 1/2 + sign(u) (1/2 - r)
-        const float2 h = add2(both(0.5f), make_float2(-r.x, -r.y));
-        slope = add2(both(0.5f), make_float2(with_sign_of(h.x, u.x), with_sign_of(h.y, u.y)));
+        // A choice rather than 1/2 + sign(u) (1/2 - r), in which r below 0 would lose what lies under 3e-8.
+        const float2 h = add2(both(1.f), make_float2(-r.x, -r.y));
+        slope = make_float2(u.x < 0.f ? r.x : h.x, u.y < 0.f ? r.y : h.y);
         y = fma2(minus, q, make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
     }
 }
