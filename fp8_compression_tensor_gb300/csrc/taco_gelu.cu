@@ -34,17 +34,17 @@ __device__ __forceinline__ float reciprocal_fast(float v)
     return r;
 }
 
-// min(|v|, 30) that keeps a NaN.
+// |v|, for positive v at most 30, and a NaN kept.  The bound keeps +infinity from meeting the tail's zero; -infinity
+// does meet it, as in u Phi(u) = -infinity 0, and comes out as NaN.
 __device__ __forceinline__ float bounded_abs(float v)
 {
     float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(v)), "f"(30.f));
+    asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(v), "f"(30.f), "f"(-v));
     return r;
 }
 
-// Upper tail q = 1 - Phi(a) of the normal distribution for a = min(|u|, 30), and
-// E = exp(-a^2 / 2) (both are zero in binary32 from a = 14 on, so the bound
-// changes nothing and keeps an infinite u from meeting them).  q = erfc(a / sqrt
+// Upper tail q = 1 - Phi(a) of the normal distribution for a = bounded_abs(u), and
+// E = exp(-a^2 / 2) (both are zero in binary32 from a = 14 on).  q = erfc(a / sqrt
 // 2) / 2 equals E t Q(t), t = 1 / (1 + 0.3 a): erfc(z) exp(z^2) is smooth and
 // falls like 1/z, so a polynomial in t follows it on the whole half line.  Q
 // (degree 7) is a least-squares fit reweighted towards the smallest largest
@@ -100,12 +100,12 @@ __device__ __forceinline__ void gelu_both2(float2 u, float2 &y, float2 &slope)
         const float2 inner = fma2(mul2(c, c), both(6.f * kTanhA * kTanhB), both(2.f * kTanhA));
         const float2 rest = fma2(g, make_float2(-g.x, -g.y), g);          // g (1 - g)
         slope = fma2(mul2(c, inner), rest, g);
-        // A NaN does not pass the clamp.
-        if (u.x != u.x)
-            slope.x = u.x;
-        if (u.y != u.y)
-            slope.y = u.y;
         y = mul2(u, g);
+        // A NaN does not pass the clamp, and -infinity gives NaN like y.
+        if (y.x != y.x)
+            slope.x = y.x;
+        if (y.y != y.y)
+            slope.y = y.y;
     } else {
         float2 e;
         const float2 a = make_float2(bounded_abs(u.x), bounded_abs(u.y)), minus = make_float2(-a.x, -a.y);

@@ -263,7 +263,8 @@ TACO_API taco_status_t taco_layernorm_backward(const taco_layernorm_backward_arg
 /*
  * GELU of u = x + bias (binary32): y = u Phi(u), or with tanh_form
  * y = u/2 (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))), and the records of u
- * (hidden < 2^30 then).
+ * (hidden < 2^30 then).  In both forms y = +infinity and slope 1 for u =
+ * +infinity, and NaN for u = -infinity (-infinity times 0) and NaN.
  */
 typedef struct taco_gelu_args {
     const void *x;              /* in:  [rows, hidden] */
