@@ -203,8 +203,8 @@ def layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opti
               code="e4m3", stream=None) -> LayerNorm:
     """Layer norm over the last dimension of x (bf16, f16 or f32), or of
     x + residual (rounded to x's type and returned as `summed`).  weight and
-    bias share one type.  mean and rstd are float32, one per row.  With
-    checkpoint, `packed` holds the normalised rows (before weight and bias) as
+    bias share one type.  mean and rstd are float32, one per row (NaN for rows
+    of no elements).  With checkpoint, `packed` holds the normalised rows (before weight and bias) as
     8-bit records."""
     kind, rows, hidden = _first(x, "x")
     device, shape, width = x.get_device(), x.shape, (hidden,)
@@ -219,6 +219,9 @@ def layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opti
         summed = torch.empty_like(x) if residual is not None else None
         mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
+        if hidden == 0:   # no element to average: 0 / 0 (the library launches nothing)
+            for t in (mean, rstd):
+                t.fill_(math.nan)
         packed = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if checkpoint else None
         rc = _library().taco_layernorm(
             _pack_layernorm(x.data_ptr(), pr, pw, pb, y.data_ptr(), _address(summed), mean.data_ptr(), rstd.data_ptr(),

@@ -202,7 +202,8 @@ TACO_API taco_status_t taco_reduce_shards_ex(const void *const *packed_shards, i
  *     free otherwise.
  *   - Every result is the same from run to run (no floating-point atomics).
  *   - Gradients of parameters sum over rows: with rows == 0 they are zeros
- *     (the kernels that write them are launched).  hidden == 0 launches nothing.
+ *     (the kernels that write them are launched).  hidden == 0 launches nothing
+ *     and leaves mean and rstd as they are.
  *   - Workspaces hold nothing between calls; a call that gets fewer bytes than
  *     its *_workspace() query returns TACO_ERR_BAD_SHAPE.
  * ------------------------------------------------------------------------- */
