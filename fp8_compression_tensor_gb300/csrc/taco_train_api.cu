@@ -128,14 +128,17 @@ int64_t taco_layernorm_backward_workspace(int64_t rows, int64_t hidden)
 
 taco_status_t taco_layernorm_backward(const taco_layernorm_backward_args_t *a, taco_stream_t stream)
 {
-    if (!a || !type_known(a->dtype) || !type_known(a->param_dtype) || !a->x != !a->mean)
+    if (!a || !type_known(a->dtype) || !type_known(a->param_dtype))
         return TACO_ERR_BAD_OPTIONS;
     int64_t n = 0;
     taco_status_t st = check_elements(a->rows, a->hidden, &n);
-    if (st == TACO_OK && !a->x && a->rows != 0)
+    if (st == TACO_OK && !a->x && !a->mean && a->rows != 0)
         st = check_records(a->hidden, a->block, a->code);
     if (st != TACO_OK || a->hidden == 0)
         return st;
+    // Only now: of [rows, 0] x is null and mean is not.
+    if (a->rows != 0 && !a->x != !a->mean)
+        return TACO_ERR_BAD_OPTIONS;
     const bool sums = a->dweight || a->dbias;
     const int parts = column_parts(a->rows);
     const int64_t need = taco_layernorm_backward_workspace(a->rows, a->hidden);
@@ -268,7 +271,7 @@ int64_t taco_weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden)
 taco_status_t taco_weight_grad(const taco_weight_grad_args_t *a, taco_stream_t stream)
 {
     if (!a || (a->dtype != TACO_DTYPE_BF16 && a->dtype != TACO_DTYPE_F32) || !type_known(a->param_dtype) ||
-        (a->accumulate != 0 && a->accumulate != 1) || !a->shift != !a->dy_sum)
+        (a->accumulate != 0 && a->accumulate != 1))
         return TACO_ERR_BAD_OPTIONS;
     int64_t nx = 0, ny = 0, nw = 0;
     taco_status_t st = check_elements(a->rows, a->hidden, &nx);
@@ -282,6 +285,9 @@ taco_status_t taco_weight_grad(const taco_weight_grad_args_t *a, taco_stream_t s
         st = TACO_ERR_BAD_SHAPE;
     if (st != TACO_OK || nw == 0)
         return st;
+    // Only now: shift is null where hidden is 0, dy_sum where out is.
+    if (!a->shift != !a->dy_sum)
+        return TACO_ERR_BAD_OPTIONS;
     const int64_t need = taco_weight_grad_workspace(a->rows, a->out, a->hidden);
     if (!a->dweight || (a->rows != 0 && (!a->dy || !a->packed)) || (need > 0 && !a->workspace))
         return TACO_ERR_NULL_POINTER;
