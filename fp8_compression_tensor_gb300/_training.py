@@ -237,17 +237,27 @@ def layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opti
 def layernorm_backward(dy: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
                        x: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
                        packed: Optional[torch.Tensor] = None, dsummed: Optional[torch.Tensor] = None,
-                       block: int = 128, code="e4m3", bias_grad: bool = True, stream=None) -> LayerNormGrads:
+                       block: int = 128, code="e4m3", bias_grad: bool = True, stream=None,
+                       bias_dtype: Optional[torch.dtype] = None) -> LayerNormGrads:
     """Gradients of layernorm from either (x, mean), x being what was
     normalised (`summed` where there was a residual), or the records `packed`.
     dsummed, the gradient that reaches `summed` from elsewhere, is added to dx.
-    dweight and dbias (in weight's type) are None without a weight; dbias also
-    with bias_grad=False."""
+    dweight is in weight's type, and None without a weight.  dbias is in that
+    type too; the bias of a norm without a weight has its gradient in
+    bias_dtype.  It is None with neither, and with bias_grad=False."""
+    if bias_dtype is not None and bias_dtype not in DTYPES:
+        raise TypeError(f"bias_dtype must be bfloat16, float16 or float32, got {bias_dtype}")
     if (x is None) == (packed is None) or (x is None) != (mean is None):
         raise ValueError("give either x with mean, or packed")
     kind, rows, hidden = _first(dy, "dy")
     device, shape, stats = dy.get_device(), dy.shape, dy.shape[:-1]
-    pdtype = _param_type(weight, "weight")
+    if weight is None:
+        pdtype = bias_dtype or torch.float32
+    else:
+        pdtype = _param_type(weight, "weight")
+        if bias_dtype is not None and bias_dtype is not pdtype:
+            raise TypeError(f"bias_dtype must be weight's type {pdtype}, got {bias_dtype}")
+    bias_grad = bias_grad and (weight is not None or bias_dtype is not None)
     prstd = _tensor(rstd, "rstd", device, torch.float32, stats)
     px = _tensor(x, "x", device, dy.dtype, shape)
     pmean = _tensor(mean, "mean", device, torch.float32, stats)
@@ -260,9 +270,9 @@ def layernorm_backward(dy: torch.Tensor, rstd: torch.Tensor, weight: Optional[to
         dx = torch.empty_like(dy)
         dweight = dbias = ws = None
         nbytes = 0
-        if weight is not None:
-            dweight = torch.empty_like(weight)
-            dbias = torch.empty_like(weight) if bias_grad else None
+        if weight is not None or bias_grad:
+            dweight = torch.empty_like(weight) if weight is not None else None
+            dbias = torch.empty(hidden, dtype=pdtype, device=dy.device) if bias_grad else None
             nbytes = _workspace_bytes("taco_layernorm_backward_workspace", rows, hidden)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
         rc = lib.taco_layernorm_backward(
