@@ -10,7 +10,8 @@ n), and GELU's gradient gives a again for the second weight gradient.
 
     python examples/mlp_block_8bit.py            # trains a small block, prints the loss and the memory kept
 
-The linear layers are torch matrix products in bf16.
+The linear layers are torch matrix products in bf16.  The block has first
+derivatives only: its gradients come from the records, outside autograd.
 """
 import os
 import sys
@@ -31,6 +32,7 @@ class MlpBlock(torch.autograd.Function):
         return act.y @ w2.t() + b2 + norm.summed
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         xhat, rstd, u, gamma, beta, w1, w2 = ctx.saved_tensors
         block, code, b1_dtype, b2_dtype = ctx.options
