@@ -11,7 +11,9 @@ operators" of include/taco.h).
 A checkpoint is a uint8 tensor of compressed_bytes(rows, hidden, block) bytes
 of DS-only records with power-of-two scales;
 decompress(packed, rows, hidden, block, variant="ds_only") gives its values.
-Argument marshalling only, like _binding.
+Argument marshalling only, like _binding.  No call records an autograd graph:
+the forward and backward calls are for a torch.autograd.Function, as in
+examples/mlp_block_8bit.py.
 """
 from __future__ import annotations
 
@@ -359,7 +361,10 @@ def weight_grad(dy: torch.Tensor, packed: torch.Tensor, hidden: int, block: int 
     layer norm's weight and bias) X stands for X scale + shift; shift needs
     dy_sum, the float32 sum of dy over rows (the layer's bias gradient).  The
     result has `dtype` (float32 or bfloat16), or goes to `out`, to which
-    accumulate=True adds it."""
+    accumulate=True adds it.  The checkpoints of layernorm and gelu enter the
+    product as they are; records of compress(variant="ds_only"), whose scales
+    are no powers of two, are rounded to bfloat16 for it (2^-9 of a value at
+    most)."""
     kind, rows, features = _first(dy, "dy")
     if kind != 0:
         raise TypeError(f"dy must be torch.bfloat16, got {dy.dtype}")

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kWideThreads) taco_norm_wide_kernel(NormArgs a
             }
             return h;
         };
-        // f(c, j) for the lane's vectors; j numbers the two of a step
+        // f(c) for the lane's vectors, c their first column
         auto each = [&](auto f) {
             for (int64_t base = warp * 512; base < C; base += kWideThreads * 16)
 #pragma unroll

@@ -147,16 +147,6 @@ __device__ __forceinline__ void store_raw8(T *p, const Raw8<T> &r)
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// Rounds to T and stores eight consecutive elements.
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&f)[8])
-{
-    const Raw8<T> r = pack8(f, static_cast<const T *>(nullptr));
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); i++)
-        reinterpret_cast<uint4 *>(p)[i] = r.v[i];
-}
-
 // Eight consecutive parameters of run-time type from i on (i a multiple of 8).
 __device__ __forceinline__ void load_param8(const void *p, int dtype, int64_t i, float (&f)[8])
 {

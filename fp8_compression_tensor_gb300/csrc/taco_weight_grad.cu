@@ -797,6 +797,8 @@ cudaError_t init_weight_grad()
 // into how many.  76 pairs take the tiles in waves; what is left for the last
 // wave is cut so that all pairs have work, down to 512 rows a range: 8192 x 4096
 // x 4096 (256 tiles, 28 of them in the last wave) takes 197 us against 211 whole.
+// The pairs of a GB300, not of the current device: the workspace query that shares
+// the plan looks at none.  With another count the plan is only less even.
 constexpr int64_t kPairs = 76;
 
 struct WgTiles {
