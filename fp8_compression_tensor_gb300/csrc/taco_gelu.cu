@@ -9,6 +9,7 @@
 // the tanh form's slope; dbias = sum over rows of dx; y again when the next
 // weight gradient needs it.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "taco_kernels.h"
@@ -102,12 +103,13 @@ __device__ __forceinline__ void gelu_both2(float2 u, float2 &y, float2 &slope)
         const float2 inner = fma2(mul2(c, c), both(6.f * kTanhA * kTanhB), both(2.f * kTanhA));
         const float2 rest = fma2(g, make_float2(-g.x, -g.y), g);          // g (1 - g)
         slope = fma2(mul2(c, inner), rest, g);
+        // What is not above -infinity gives NaN, as y = u g does; it does not pass the clamp.  Asked of u: asked of y, 8192 x
+        // 16384 takes 169 us against 160.
+        if (!(u.x >= -FLT_MAX))
+            slope.x = __uint_as_float(0x7fc00000u);
+        if (!(u.y >= -FLT_MAX))
+            slope.y = __uint_as_float(0x7fc00000u);
         y = mul2(u, g);
-        // A NaN does not pass the clamp, and -infinity gives NaN like y.
-        if (y.x != y.x)
-            slope.x = y.x;
-        if (y.y != y.y)
-            slope.y = y.y;
     } else {
         float2 e;
         const float2 a = make_float2(bounded_abs(u.x), bounded_abs(u.y)), minus = make_float2(-a.x, -a.y);
