@@ -35,8 +35,8 @@ __device__ __forceinline__ float reciprocal_fast(float v)
     return r;
 }
 
-// |v|, for positive v at most 30, and a NaN kept.  The bound keeps +infinity from meeting the tail's zero; -infinity
-// does meet it, as in u Phi(u) = -infinity 0, and comes out as NaN.
+// |v|, for positive v at most 30, and a NaN kept.  In the gradient the bound keeps +infinity from meeting the tail's
+// zero; -infinity does meet it, as in u Phi(u) = -infinity 0, and comes out as NaN.
 __device__ __forceinline__ float bounded_abs(float v)
 {
     float r;
@@ -44,7 +44,7 @@ __device__ __forceinline__ float bounded_abs(float v)
     return r;
 }
 
-// Upper tail q = 1 - Phi(a) of the normal distribution for a = bounded_abs(u), and
+// Upper tail q = 1 - Phi(a) of the normal distribution for a = |u|, and
 // E = exp(-a^2 / 2), which the exponential flushes to zero below 2^-126 (a above
 // 13.2).  q = erfc(a / sqrt 2) / 2 equals E t Q(t), t = 1 / (1 + 0.3 a): erfc(z)
 // exp(z^2) is smooth and falls like 1/z, so a polynomial in t follows it on the
@@ -54,8 +54,10 @@ __device__ __forceinline__ float bounded_abs(float v)
 // relative error grows with the exponent's rounding, which weighs a^2 / 2: measured
 // 7e-7 up to a = 4, 3.3e-6 up to 9, 7e-6 up to 13.  One exponential and one
 // reciprocal serve Phi and, in the gradient, the density too.
-//   gelu(u)  = max(u, 0) - a q
+//   gelu(u)  = u Phi(u) = u q for u < 0 and u (1 - q) otherwise, which is max(u, 0) - a q
 //   gelu'(u) = Phi(u) + u phi(u) = r for u < 0 and 1 - r otherwise, r = q - a phi(a)
+// The value alone takes the first form: 8192 x 16384 bf16 with records 132 us against 134.  The gradient takes the
+// second one, whose bounded a it has.
 __device__ __forceinline__ float2 normal_tail2(float2 a, float2 &e)
 {
     const float2 x = mul2(mul2(a, a), both(-0.5f * kLog2e));
@@ -87,9 +89,8 @@ __device__ __forceinline__ float2 gelu_value2(float2 u)
     if (TANH)
         return mul2(u, tanh_gate2(u));
     float2 e;
-    const float2 a = make_float2(bounded_abs(u.x), bounded_abs(u.y));
-    const float2 q = normal_tail2(a, e);
-    return fma2(make_float2(-a.x, -a.y), q, make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
+    const float2 q = normal_tail2(make_float2(fabsf(u.x), fabsf(u.y)), e), p = add2(both(1.f), make_float2(-q.x, -q.y));
+    return mul2(u, make_float2(u.x < 0.f ? q.x : p.x, u.y < 0.f ? q.y : p.y));
 }
 
 // gelu(u) and its slope.
