@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) taco_gelu_grad_kernel(GeluGra
             for (int i = 0; i < 4; i++) {
                 float2 slope = both(0.f);
                 // The second condition always holds.  As a branch it keeps the compiler from interleaving the four pairs of the
-                // erf form, which ran 8192 x 16384 in 177 us; one after the other they take 162.
+                // erf form, which takes 8192 x 16384 bf16 166 us and 8192 x 8192 f32 181; one after the other 162 and 142.
                 if (TANH || a.tanh_form == 0)
                     gelu_both2<TANH>(mul2(q.v[i], both(s)), y.v[i], slope);
                 d.v[i] = mul2(g.v[i], slope);
