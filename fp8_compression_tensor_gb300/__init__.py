@@ -19,6 +19,13 @@ activations and the gradients that read them):
     g = gelu_backward(dy, r.packed, bias_dtype=torch.float32)
     dw = weight_grad(dy, packed, hidden)
 
+and those of a gated feed-forward block behind an RMS norm:
+
+    r = rmsnorm(x, weight, residual=None, checkpoint=True)
+    g = rmsnorm_backward(dy, r.rstd, weight, packed=r.packed)
+    r = gated_linear(x, weight, activation="silu", checkpoint=True)
+    g = gated_linear_backward(dy, r.packed, weight)
+
 The kernels live in libtaco_gb300.so (C ABI: include/taco.h); this package
 only marshals arguments.  Build the library with
 `python -m fp8_compression_tensor_gb300.build`.
@@ -26,10 +33,13 @@ only marshals arguments.  Build the library with
 from ._binding import (CODES, LIBRARY_PATH, MAX_SHARDS, STATUS, SUPPORTED_BLOCKS, VARIANTS,  # noqa: F401
                        TacoError, compress, compressed_bytes, decompress, device_status, load_library, raw_call,
                        reduce_shards, selftest_encode_bits)
+from ._gated import (ACTIVATIONS, GatedLinear, GatedLinearGrads, RmsNorm, RmsNormGrads, gated_linear,  # noqa: F401
+                     gated_linear_backward, rmsnorm, rmsnorm_backward)
 from ._training import (Gelu, GeluGrads, LayerNorm, LayerNormGrads, gelu, gelu_backward, layernorm,  # noqa: F401
                         layernorm_backward, weight_grad)
 
 __all__ = ["compress", "decompress", "reduce_shards", "compressed_bytes", "device_status", "load_library",
            "TacoError", "LIBRARY_PATH", "MAX_SHARDS", "SUPPORTED_BLOCKS", "STATUS", "VARIANTS", "CODES",
            "raw_call", "selftest_encode_bits", "layernorm", "layernorm_backward", "gelu", "gelu_backward", "weight_grad",
-           "LayerNorm", "LayerNormGrads", "Gelu", "GeluGrads"]
+           "LayerNorm", "LayerNormGrads", "Gelu", "GeluGrads", "rmsnorm", "rmsnorm_backward", "gated_linear", "gated_linear_backward",
+           "RmsNorm", "RmsNormGrads", "GatedLinear", "GatedLinearGrads", "ACTIVATIONS"]

@@ -22,8 +22,8 @@
 
 namespace taco {
 
-// Fault flag of the weight gradient, next to those of the codec (taco_device.cuh).
-constexpr uint32_t kFaultWeightGrad = 16u;
+// Fault flags of the weight gradient and the gated layer, next to those of the codec (taco_device.cuh).
+constexpr uint32_t kFaultWeightGrad = 16u, kFaultGated = 32u;
 
 // ---------------------------------------------------------------------------
 // Typed elements

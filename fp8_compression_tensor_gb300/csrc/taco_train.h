@@ -55,6 +55,53 @@ struct NormGradArgs {
     int param_dtype, block, code, nparts;
 };
 
+struct RmsArgs {
+    const void *x, *residual, *weight;          // residual, weight may be null
+    void *y, *summed;                           // y null: records of it; summed non-null exactly with residual
+    float *rstd;
+    uint8_t *packed, *packed_y;                 // null: no records
+    int64_t rows, hidden;
+    float eps;
+    int param_dtype, block, code;
+};
+
+struct RmsGradArgs {
+    const void *dy, *x, *weight, *dsummed;      // x null: from records
+    const float *rstd;
+    const uint8_t *packed;
+    void *dx;
+    float *parts;                               // [parts][hidden] column sums of dy * xhat; null: none wanted
+    int64_t rows, hidden;
+    int param_dtype, block, code, nparts;
+};
+
+struct GatedArgs {
+    const void *x, *weight, *bias;              // bias may be null
+    void *y;
+    uint8_t *packed;                            // null: no records
+    void *workspace;                            // gated_workspace() bytes
+    int64_t rows, inner, hidden;
+    int dtype, param_dtype, activation, block, code;
+};
+
+struct GatedGradArgs {
+    const void *dy;
+    const uint8_t *packed;
+    void *dz, *y;                               // y may be null
+    float *parts;                               // [parts][2 inner] column sums of dz; null: none wanted
+    int64_t rows, inner;
+    int activation, block, code, nparts;
+};
+
+// dx = dz W
+struct GatedInputGradArgs {
+    const void *dz, *weight;
+    void *dx;
+    void *workspace;                            // gated_input_grad_workspace() bytes
+    int64_t rows, inner, hidden;
+    int dtype;
+};
+
 struct GeluArgs {
     const void *x, *bias;
     void *y;
@@ -87,12 +134,26 @@ struct WeightGradArgs {
 cudaError_t init_weight_grad();
 cudaError_t init_norm();
 cudaError_t init_norm_grad();
+cudaError_t init_rms();
+cudaError_t init_rms_grad();
+cudaError_t init_gated();
 
 cudaError_t launch_norm(int dtype, const NormArgs &a, int sms, cudaStream_t stream);
 // The gradient launches set nparts to the number of row chunks they use (at most what the caller gives).
 cudaError_t launch_norm_grad(int dtype, NormGradArgs *a, int sms, cudaStream_t stream);
 cudaError_t launch_gelu(int dtype, const GeluArgs &a, int sms, cudaStream_t stream);
 cudaError_t launch_gelu_grad(int dtype, GeluGradArgs *a, int sms, cudaStream_t stream);
+
+cudaError_t launch_rms(int dtype, const RmsArgs &a, int sms, cudaStream_t stream);
+cudaError_t launch_rms_grad(int dtype, RmsGradArgs *a, int sms, cudaStream_t stream);
+cudaError_t launch_gated_grad(int dtype, GatedGradArgs *a, int sms, cudaStream_t stream);
+
+// Workspaces of the gated layer's products and the range that their kernels address.
+int64_t gated_workspace(int64_t rows, int64_t inner, int64_t hidden);
+int64_t gated_input_grad_workspace(int64_t rows, int64_t inner, int64_t hidden);
+bool gated_in_range(int64_t rows, int64_t inner, int64_t hidden);
+cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
+cudaError_t launch_gated_input_grad(const GatedInputGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
 
 // Workspace of a weight gradient and the range its kernels address.
 int64_t weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden);

@@ -77,9 +77,42 @@ taco_status_t training_device(DeviceState **out)
             e = init_norm();
         if (e == cudaSuccess)
             e = init_norm_grad();
+        if (e == cudaSuccess)
+            e = init_rms();
+        if (e == cudaSuccess)
+            e = init_rms_grad();
+        if (e == cudaSuccess)
+            e = init_gated();
         dev->train_error = e;
     });
     return dev->train_error == cudaSuccess ? TACO_OK : cuda_fail(dev->train_error);
+}
+
+// The gated layer's sizes: elements of [rows, inner], [rows, hidden] and [2 inner, hidden] in range.
+taco_status_t check_gated(int64_t rows, int64_t inner, int64_t hidden, int64_t *ny, int64_t *nx, int64_t *nw)
+{
+    taco_status_t st = check_elements(rows, inner, ny);
+    if (st == TACO_OK)
+        st = check_elements(rows, hidden, nx);
+    if (st == TACO_OK)
+        st = check_elements(inner, hidden, nw);
+    if (st != TACO_OK || !gated_in_range(rows, inner, hidden))
+        return TACO_ERR_BAD_SHAPE;
+    *nw *= 2;
+    return TACO_OK;
+}
+
+taco_status_t check_gated_records(int64_t inner, int block, int code)
+{
+    if (code_known(code) && block > 128 && block_supported(block))
+        return TACO_ERR_UNSUPPORTED_BLOCK;
+    return check_records(inner, block, code);
+}
+
+bool gated_options(int dtype, int param_dtype, int activation)
+{
+    return (dtype == TACO_DTYPE_BF16 || dtype == TACO_DTYPE_F16) && type_known(param_dtype) &&
+           activation >= TACO_ACTIVATION_SILU && activation <= TACO_ACTIVATION_GELU_TANH;
 }
 
 taco_status_t done(cudaError_t e) { return e == cudaSuccess ? TACO_OK : cuda_fail(e); }
@@ -310,6 +343,203 @@ taco_status_t taco_weight_grad(const taco_weight_grad_args_t *a, taco_stream_t s
                            static_cast<float *>(a->workspace), a->rows, a->out, a->hidden, a->dtype, a->param_dtype,
                            a->accumulate, a->block, a->code};
     return done(launch_weight_grad(k, dev->fault, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+taco_status_t taco_rmsnorm(const taco_rmsnorm_args_t *a, taco_stream_t stream)
+{
+    if (!a || !type_known(a->dtype) || !type_known(a->param_dtype) || !(a->eps >= 0.f) || !a->residual != !a->summed)
+        return TACO_ERR_BAD_OPTIONS;
+    int64_t n = 0;
+    taco_status_t st = check_elements(a->rows, a->hidden, &n);
+    if (st == TACO_OK && (a->packed || a->packed_y))
+        st = check_records(a->hidden, a->block, a->code);
+    if (st != TACO_OK || n == 0)
+        return st;
+    if (a->y && a->packed_y)
+        return TACO_ERR_BAD_OPTIONS;
+    if (!a->x || (!a->y && !a->packed_y) || !a->rstd)
+        return TACO_ERR_NULL_POINTER;
+    const int64_t bytes = n * type_bytes(a->dtype), record = a->packed || a->packed_y ? record_bytes(n, a->block) : 0;
+    const Span spans[] = {{a->x, bytes, false},
+                          {a->residual, bytes, false},
+                          {a->weight, a->hidden * type_bytes(a->param_dtype), false},
+                          {a->y, bytes, true},
+                          {a->summed, bytes, true},
+                          {a->rstd, 4 * a->rows, true},
+                          {a->packed, record, true},
+                          {a->packed_y, record, true}};
+    if ((st = check_spans(spans)) != TACO_OK)
+        return st;
+    DeviceState *dev = nullptr;
+    if ((st = training_device(&dev)) != TACO_OK)
+        return st;
+    const RmsArgs k{a->x,    a->residual, a->weight, a->y,  a->summed,      a->rstd,  static_cast<uint8_t *>(a->packed),
+                    static_cast<uint8_t *>(a->packed_y), a->rows, a->hidden, a->eps, a->param_dtype, a->block, a->code};
+    return done(launch_rms(a->dtype, k, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t taco_rmsnorm_backward_workspace(int64_t rows, int64_t hidden)
+{
+    int64_t n = 0;
+    if (check_elements(rows, hidden, &n) != TACO_OK)
+        return -1;
+    return 4 * column_parts(rows) * hidden;
+}
+
+taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t *a, taco_stream_t stream)
+{
+    if (!a || !type_known(a->dtype) || !type_known(a->param_dtype))
+        return TACO_ERR_BAD_OPTIONS;
+    int64_t n = 0;
+    taco_status_t st = check_elements(a->rows, a->hidden, &n);
+    if (st == TACO_OK && a->packed && a->rows != 0)
+        st = check_records(a->hidden, a->block, a->code);
+    if (st != TACO_OK || a->hidden == 0)
+        return st;
+    const int64_t need = taco_rmsnorm_backward_workspace(a->rows, a->hidden);
+    if (a->rows != 0) {
+        if (a->x && a->packed)
+            return TACO_ERR_BAD_OPTIONS;
+        if (!a->dy || !a->rstd || !a->dx || (!a->x && !a->packed) || (a->dweight && !a->workspace))
+            return TACO_ERR_NULL_POINTER;
+        if (a->dweight && a->workspace_bytes < need)
+            return TACO_ERR_BAD_SHAPE;
+    } else if (!a->dweight) {
+        return TACO_OK;
+    }
+    const int64_t bytes = n * type_bytes(a->dtype), pbytes = a->hidden * type_bytes(a->param_dtype);
+    const Span spans[] = {{a->dy, bytes, false},
+                          {a->x, bytes, false},
+                          {a->rstd, 4 * a->rows, false},
+                          {a->packed, a->packed && a->rows != 0 ? record_bytes(n, a->block) : 0, false},
+                          {a->weight, pbytes, false},
+                          {a->dsummed, bytes, false},
+                          {a->dx, bytes, true},
+                          {a->dweight, pbytes, true},
+                          {a->dweight ? a->workspace : nullptr, need, true}};
+    if ((st = check_spans(spans)) != TACO_OK)
+        return st;
+    DeviceState *dev = nullptr;
+    if ((st = training_device(&dev)) != TACO_OK)
+        return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    float *ws = a->dweight ? static_cast<float *>(a->workspace) : nullptr;
+    RmsGradArgs k{a->dy, a->x, a->weight, a->dsummed, a->rstd, static_cast<const uint8_t *>(a->packed), a->dx,
+                  ws, a->rows, a->hidden, a->param_dtype, a->block, a->code, column_parts(a->rows)};
+    cudaError_t e = cudaSuccess;
+    if (a->rows != 0)
+        e = launch_rms_grad(a->dtype, &k, dev->sm_count, s);
+    if (e == cudaSuccess && ws)
+        e = launch_column_sums(ws, k.nparts, a->hidden, a->dweight, nullptr, a->param_dtype, s);
+    else if (e == cudaSuccess && a->dweight)   // no rows, so no workspace
+        e = launch_column_sums(nullptr, 0, a->hidden, a->dweight, nullptr, a->param_dtype, s);
+    return done(e);
+}
+
+int64_t taco_gated_linear_workspace(int64_t rows, int64_t inner, int64_t hidden)
+{
+    int64_t ny = 0, nx = 0, nw = 0;
+    if (check_gated(rows, inner, hidden, &ny, &nx, &nw) != TACO_OK)
+        return -1;
+    return gated_workspace(rows, inner, hidden);
+}
+
+taco_status_t taco_gated_linear(const taco_gated_linear_args_t *a, taco_stream_t stream)
+{
+    if (!a || !gated_options(a->dtype, a->param_dtype, a->activation))
+        return TACO_ERR_BAD_OPTIONS;
+    int64_t ny = 0, nx = 0, nw = 0;
+    taco_status_t st = check_gated(a->rows, a->inner, a->hidden, &ny, &nx, &nw);
+    if (st == TACO_OK && a->packed)
+        st = check_gated_records(a->inner, a->block, a->code);
+    if (st == TACO_OK && a->hidden == 0)
+        st = TACO_ERR_BAD_SHAPE;
+    if (st != TACO_OK || ny == 0)
+        return st;
+    const int64_t need = gated_workspace(a->rows, a->inner, a->hidden);
+    if (!a->x || !a->weight || !a->y || (need > 0 && !a->workspace))
+        return TACO_ERR_NULL_POINTER;
+    if (a->workspace_bytes < need)
+        return TACO_ERR_BAD_SHAPE;
+    const Span spans[] = {{a->x, 2 * nx, false},
+                          {a->weight, 2 * nw, false},
+                          {a->bias, 2 * a->inner * type_bytes(a->param_dtype), false},
+                          {a->y, 2 * ny, true},
+                          {a->packed, a->packed ? record_bytes(2 * ny, a->block) : 0, true},
+                          {need > 0 ? a->workspace : nullptr, need, true}};
+    if ((st = check_spans(spans)) != TACO_OK)
+        return st;
+    DeviceState *dev = nullptr;
+    if ((st = training_device(&dev)) != TACO_OK)
+        return st;
+    const GatedArgs k{a->x, a->weight, a->bias, a->y, static_cast<uint8_t *>(a->packed), a->workspace, a->rows, a->inner,
+                      a->hidden, a->dtype, a->param_dtype, a->activation, a->block, a->code};
+    return done(launch_gated(k, dev->fault, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The input gradient's workspace, then the bias gradient's.
+int64_t taco_gated_linear_backward_workspace(int64_t rows, int64_t inner, int64_t hidden)
+{
+    int64_t ny = 0, nx = 0, nw = 0;
+    if (check_gated(rows, inner, hidden, &ny, &nx, &nw) != TACO_OK)
+        return -1;
+    return (hidden > 0 && rows > 0 ? gated_input_grad_workspace(rows, inner, hidden) : 0) + 8 * column_parts(rows) * inner;
+}
+
+taco_status_t taco_gated_linear_backward(const taco_gated_linear_backward_args_t *a, taco_stream_t stream)
+{
+    if (!a || !gated_options(a->dtype, a->param_dtype, a->activation))
+        return TACO_ERR_BAD_OPTIONS;
+    int64_t ny = 0, nx = 0, nw = 0;
+    taco_status_t st = check_gated(a->rows, a->inner, a->hidden, &ny, &nx, &nw);
+    if (st == TACO_OK)
+        st = check_gated_records(a->inner, a->block, a->code);
+    if (st == TACO_OK && a->inner == 0)
+        st = TACO_ERR_BAD_SHAPE;
+    if (st != TACO_OK)
+        return st;
+    const bool input = a->weight || a->dx;
+    const int64_t product = input && a->rows > 0 ? gated_input_grad_workspace(a->rows, a->inner, a->hidden) : 0;
+    const int64_t sums = a->dbias ? 8 * column_parts(a->rows) * a->inner : 0, need = product + sums;
+    if (a->rows != 0) {
+        if (input && a->hidden == 0)
+            return TACO_ERR_BAD_SHAPE;
+        if (!a->weight != !a->dx)
+            return TACO_ERR_BAD_OPTIONS;
+        if (!a->dy || !a->packed || !a->dz || (need > 0 && !a->workspace))
+            return TACO_ERR_NULL_POINTER;
+        if (a->workspace_bytes < need)
+            return TACO_ERR_BAD_SHAPE;
+    } else if (!a->dbias) {
+        return TACO_OK;
+    }
+    const Span spans[] = {{a->dy, 2 * ny, false},
+                          {a->packed, record_bytes(2 * ny, a->block), false},
+                          {a->weight, 2 * nw, false},
+                          {a->dz, 4 * ny, true},
+                          {a->dx, 2 * nx, true},
+                          {a->y, 2 * ny, true},
+                          {a->dbias, 2 * a->inner * type_bytes(a->param_dtype), true},
+                          {need > 0 ? a->workspace : nullptr, need, true}};
+    if ((st = check_spans(spans)) != TACO_OK)
+        return st;
+    DeviceState *dev = nullptr;
+    if ((st = training_device(&dev)) != TACO_OK)
+        return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    float *parts = sums > 0 ? reinterpret_cast<float *>(static_cast<uint8_t *>(a->workspace) + product) : nullptr;
+    GatedGradArgs k{a->dy, static_cast<const uint8_t *>(a->packed), a->dz, a->y, parts, a->rows, a->inner,
+                    a->activation, a->block, a->code, 0};
+    cudaError_t e = cudaSuccess;
+    if (a->rows != 0)
+        e = launch_gated_grad(a->dtype, &k, dev->sm_count, s);
+    if (e == cudaSuccess && a->rows != 0 && a->dx) {
+        const GatedInputGradArgs g{a->dz, a->weight, a->dx, a->workspace, a->rows, a->inner, a->hidden, a->dtype};
+        e = launch_gated_input_grad(g, dev->fault, dev->sm_count, s);
+    }
+    if (e == cudaSuccess && a->dbias)
+        e = launch_column_sums(parts, k.nparts, 2 * a->inner, a->dbias, nullptr, a->param_dtype, s);
+    return done(e);
 }
 
 }  // extern "C"

@@ -181,7 +181,8 @@ TACO_API taco_status_t taco_reduce_shards_ex(const void *const *packed_shards, i
 /* ------------------------------------------------------------------------- *
  * Training operators around the compressed tensors: the layer norm behind a
  * tensor-parallel AllReduce, GELU, and 8-bit checkpoints of the activations
- * that a training step keeps from its forward to its backward pass.
+ * that a training step keeps from its forward to its backward pass; and for
+ * gated feed-forward blocks the RMS norm and the gated linear layer.
  *
  * A checkpoint is a packed buffer of DS-only records (taco_variant_t) with
  * alpha = 1 and a scale that is a power of two: for a block's values u with
@@ -325,10 +326,119 @@ TACO_API int64_t taco_weight_grad_workspace(int64_t rows, int64_t out, int64_t h
 TACO_API taco_status_t taco_weight_grad(const taco_weight_grad_args_t *args, taco_stream_t stream);
 
 /*
+ * Root-mean-square norm of h = x, or of h = x + residual rounded to `dtype`:
+ *   rstd = 1 / sqrt(sum h^2 / hidden + eps), xhat = h rstd, y = xhat weight.
+ * y is a tensor, or 8-bit records (packed_y) made from the binary32 values, for a
+ * y that is sent or stored.  packed holds the records of xhat, the checkpoint
+ * of the calls below.
+ */
+typedef struct taco_rmsnorm_args {
+    const void *x;              /* in:  [rows, hidden] */
+    const void *residual;       /* in:  [rows, hidden], or NULL */
+    const void *weight;         /* in:  [hidden] of param_dtype; NULL: 1 */
+    void *y;                    /* out: [rows, hidden]; NULL exactly when packed_y is not */
+    void *summed;               /* out: h, [rows, hidden]; non-NULL exactly when residual is */
+    float *rstd;                /* out: [rows] */
+    void *packed;               /* out: records of xhat, or NULL */
+    void *packed_y;             /* out: records of y, or NULL */
+    int64_t rows, hidden;
+    float eps;                  /* >= 0 */
+    int dtype, param_dtype;     /* taco_dtype_t */
+    int block, code;            /* of the records; read only when there are some */
+} taco_rmsnorm_args_t;
+
+TACO_API taco_status_t taco_rmsnorm(const taco_rmsnorm_args_t *args, taco_stream_t stream);
+
+/*
+ * Gradients of the RMS norm, with a = dy weight and c = sum a xhat / hidden:
+ * dx = rstd (a - xhat c) + dsummed, dweight = sum over rows of dy xhat.  xhat
+ * comes from x (what was normalised: the forward call's `summed` where it had a
+ * residual) as x rstd, or from the records of the forward call.
+ */
+typedef struct taco_rmsnorm_backward_args {
+    const void *dy;             /* in:  [rows, hidden] */
+    const void *x;              /* in:  [rows, hidden], or NULL to read the records */
+    const float *rstd;          /* in:  [rows] */
+    const void *packed;         /* in:  records of xhat; non-NULL exactly when x is NULL */
+    const void *weight;         /* in:  [hidden], or NULL */
+    const void *dsummed;        /* in:  [rows, hidden] added to dx, or NULL */
+    void *dx;                   /* out: [rows, hidden] */
+    void *dweight;              /* out: [hidden] of param_dtype, or NULL */
+    void *workspace;            /* needed when dweight is given */
+    int64_t workspace_bytes;
+    int64_t rows, hidden;
+    int dtype, param_dtype;
+    int block, code;            /* of the records */
+} taco_rmsnorm_backward_args_t;
+
+TACO_API int64_t taco_rmsnorm_backward_workspace(int64_t rows, int64_t hidden);   /* bytes; -1: bad shape */
+TACO_API taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t *args, taco_stream_t stream);
+
+/*
+ * Gated linear layer: both projections of a gated feed-forward block, the
+ * activation and the product.  With z = x W^T + bias, W's first `inner` rows the
+ * gate's and the others the up projection's,
+ *   y = act(z_gate) z_up,  and the records of z, [rows, 2 inner] (inner % block == 0
+ * then, blocks 32, 64 and 128).  The activation: silu(g) = g / (1 + exp(-g)),
+ * or GELU in either form.  bf16 and f16; x and W have one type.
+ * hidden >= 1.  rows == 0 or inner == 0 launches nothing.
+ */
+typedef enum taco_activation {
+    TACO_ACTIVATION_SILU = 0,
+    TACO_ACTIVATION_GELU = 1,
+    TACO_ACTIVATION_GELU_TANH = 2
+} taco_activation_t;
+
+typedef struct taco_gated_linear_args {
+    const void *x;              /* in:  [rows, hidden] */
+    const void *weight;         /* in:  [2 inner, hidden] of dtype */
+    const void *bias;           /* in:  [2 inner] of param_dtype, or NULL */
+    void *y;                    /* out: [rows, inner] */
+    void *packed;               /* out: records of z, or NULL */
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t rows, inner, hidden;
+    int dtype, param_dtype;     /* dtype: BF16 or F16 */
+    int activation;             /* taco_activation_t */
+    int block, code;            /* of the records; read only when packed is non-NULL */
+} taco_gated_linear_args_t;
+
+TACO_API int64_t taco_gated_linear_workspace(int64_t rows, int64_t inner, int64_t hidden);   /* bytes; -1: bad shape */
+TACO_API taco_status_t taco_gated_linear(const taco_gated_linear_args_t *args, taco_stream_t stream);
+
+/*
+ * Gradients of the gated linear layer with z from its records:
+ *   dz_gate = dy z_up act'(z_gate), dz_up = dy act(z_gate), dx = dz W,
+ *   dbias = sum over rows of dz (before rounding), and y again.
+ * dx is the product of dz as it is written (rounded to dtype).  The weight's
+ * gradient dz^T X is taco_weight_grad's (`out` = 2 inner).  inner >= 1, and
+ * hidden >= 1 where dx is wanted.
+ */
+typedef struct taco_gated_linear_backward_args {
+    const void *dy;             /* in:  [rows, inner] */
+    const void *packed;         /* in:  records of z */
+    const void *weight;         /* in:  [2 inner, hidden] of dtype; non-NULL exactly when dx is */
+    void *dz;                   /* out: [rows, 2 inner] */
+    void *dx;                   /* out: [rows, hidden], or NULL */
+    void *y;                    /* out: [rows, inner], or NULL */
+    void *dbias;                /* out: [2 inner] of param_dtype, or NULL */
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t rows, inner, hidden;
+    int dtype, param_dtype;     /* dtype: BF16 or F16 */
+    int activation;
+    int block, code;
+} taco_gated_linear_backward_args_t;
+
+/* Bytes for a call that wants dbias and, with hidden > 0, dx; -1: bad shape. */
+TACO_API int64_t taco_gated_linear_backward_workspace(int64_t rows, int64_t inner, int64_t hidden);
+TACO_API taco_status_t taco_gated_linear_backward(const taco_gated_linear_backward_args_t *args, taco_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's fault
  * flags (bit 0: compress, bit 1: decompress, bit 2: shard reduce gave up
  * waiting for a copy or a tile assignment; bit 3: the self-test below; bit 4:
- * weight gradient).
+ * weight gradient; bit 5: gated linear layer).
  * *flags_out (may be NULL) receives them.  Returns TACO_ERR_DEVICE_FAULT if any
  * flag was set, TACO_ERR_CUDA if a CUDA call failed, TACO_OK otherwise.
  */
