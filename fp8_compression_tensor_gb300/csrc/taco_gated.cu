@@ -2,141 +2,619 @@
 // product and the 8-bit checkpoint of the projections) and its input's gradient,
 // for GB300 (sm_103a).
 //
-//   z = x W^T + bias,  y = act(z_gate) z_up,  dx = dz W
+//   z = x W^T + bias,  y = act(z_gate) z_up, records of z;     dx = dz W
+//
+// A pair of CTAs (a cluster of two) computes a tile of 256 rows with
+// tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 16): of the layer 128 columns of
+// the gate and the same 128 of the up projection, of dx 256 columns.  Each CTA
+// holds 128 rows of A and of B.  For the layer the even CTA loads the gate's rows
+// of W and the odd one the up projection's, so one product gives both halves of
+// every element to the same thread of the epilogue, and z never leaves the chip
+// but as records.  Operands come by TMA (128-byte swizzle; x, W and dz K-major, for
+// dx W N-major) in five stages of 64 along K; all copies of a stage count on the
+// even CTA's barrier.  Two accumulators of 256 tensor-memory columns take turns, so
+// the epilogue of a tile runs beside the next one's products.
+//
+// Roles (384 threads): warp 0 loads, warp 1 of the even CTA issues the products,
+// warp 2 owns tensor memory, warps 4-11 are the epilogue: warp w reads lanes 32 (w
+// % 4) .., a row a thread.
 #include <algorithm>
 #include <climits>
 
 #include "taco_activation.cuh"
 #include "taco_kernels.h"
+#include "taco_pair.cuh"
 
 namespace taco {
 namespace {
 
-// out[M, N] = A[M, K] B, B stored as [N, K] or (BT) as [K, N]: tiles of 64 x 64, 4 x 4 a thread, sums in binary32.
-template <typename T, typename O, bool BT>
-__global__ void __launch_bounds__(256) taco_gated_product_kernel(const T *a, const T *b, O *out, int64_t M, int64_t N, int64_t K)
-{
-    __shared__ float sa[16][65], sb[16][65];
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int64_t tiles_n = (N + 63) / 64, tiles = tiles_n * ((M + 63) / 64);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t m0 = t / tiles_n * 64, n0 = t % tiles_n * 64;
-        float acc[4][4] = {};
-        for (int64_t k0 = 0; k0 < K; k0 += 16) {
-            for (int i = threadIdx.x; i < 1024; i += 256) {
-                const int64_t m = m0 + i / 16, k = k0 + i % 16;
-                sa[i % 16][i / 16] = m < M && k < K ? to_float(a[m * K + k]) : 0.f;
-                const int64_t n = n0 + (BT ? i % 64 : i / 16), kb = k0 + (BT ? i / 64 : i % 16);
-                sb[BT ? i / 64 : i % 16][BT ? i % 64 : i / 16] = n < N && kb < K ? to_float(b[BT ? kb * N + n : n * K + kb]) : 0.f;
-            }
-            __syncthreads();
-            for (int k = 0; k < 16; k++)
-                for (int i = 0; i < 4; i++)
-                    for (int j = 0; j < 4; j++)
-                        acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
-            __syncthreads();
-        }
-        for (int i = 0; i < 4; i++)
-            for (int j = 0; j < 4; j++)
-                if (m0 + ty + 16 * i < M && n0 + tx + 16 * j < N)
-                    out[(m0 + ty + 16 * i) * N + n0 + tx + 16 * j] = from_float<O>(acc[i][j]);
+constexpr int kTileM = 256;                   // rows of a pair's tile
+constexpr int kStageK = 64;                   // of the sum per pipeline stage
+constexpr int kStages = 5;
+constexpr int kOperandBytes = 128 * kStageK * 2, kStageBytes = 2 * kOperandBytes;   // of one CTA
+constexpr int kHalfBytes = 64 * kStageK * 2;                                        // 64 columns of an N-major B
+constexpr int kWarpBytes = 8192;              // an epilogue warp's buffer for what it writes
+constexpr int kThreads = 384;
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + 8 * kWarpBytes;
+constexpr int kInputGrad = -1;                // in the place of an activation: dx = dz W
+
+struct Barriers {
+    uint64_t full[kStages];       // even CTA: both CTAs' A and B of the stage have landed
+    uint64_t empty[kStages];      // the stage's products are done
+    uint64_t acc_full[2];         // an accumulator is complete
+    uint64_t acc_empty[2];        // even CTA: both CTAs have read the accumulator
+    uint64_t drained;             // even CTA, after a wait that gave up: the products issued so far are done
+    uint32_t tmem;
+};
+
+// The grid's work.  Tiles go to the CTA pairs in groups of `group_m` row tiles,
+// rows fastest, so that the pairs that run at a time share rows of A and of B in
+// L2; the last `tail` tiles, which would leave pairs idle, are cut into `splits`
+// ranges of K each, whose sums go to `parts` and are joined by a second kernel.
+struct Plan {
+    int64_t units, whole;             // work items, and how many of them are whole tiles
+    int tiles_m, tiles_n, group_m, stages_total, tail, splits;
+    __host__ __device__ void tile(int64_t t, int &m, int &n) const
+    {
+        const int64_t per_group = static_cast<int64_t>(group_m) * tiles_n, g = t / per_group, r = t - g * per_group;
+        const int rows = min(group_m, tiles_m - static_cast<int>(g) * group_m);
+        m = static_cast<int>(g) * group_m + static_cast<int>(r % rows);
+        n = static_cast<int>(r / rows);
     }
+    // part: index of the tile's sums in `parts`, or -1 for a whole tile
+    __device__ void at(int64_t u, int &m, int &n, int64_t &part, int &first, int &count) const
+    {
+        int64_t t = u;
+        first = 0;
+        count = stages_total;
+        part = -1;
+        if (u >= whole) {
+            part = u - whole;
+            const int split = static_cast<int>(part / tail);
+            t = whole + part - static_cast<int64_t>(split) * tail;
+            first = static_cast<int>(static_cast<int64_t>(stages_total) * split / splits);
+            count = static_cast<int>(static_cast<int64_t>(stages_total) * (split + 1) / splits) - first;
+        }
+        tile(t, m, n);
+    }
+};
+
+struct TileArgs {
+    void *out;                        // y or dx, [rows, width]
+    uint8_t *packed;
+    const void *bias;
+    float *parts;
+    int64_t rows, width;
+    int param_dtype, block, code, f16, tma_out;
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int f16)
+{
+    return f16 ? float2_to_f16x2(lo, hi) : float2_to_bf16x2(lo, hi);
 }
 
-// y and the records of z from z as binary32: a warp takes 256 columns of a row.
-template <typename T, int ACT>
-__global__ void __launch_bounds__(256) taco_gated_finish_kernel(GatedArgs a, const float *z)
+// A warp's 32 rows of 64 16-bit columns: its buffer holds them in the 128-byte
+// swizzle of the output's tensor map.
+__device__ __forceinline__ void stage_row32(uint32_t buffer, int lane, int chunk, const float (&v)[32], int f16)
 {
-    grid_launch_dependents();
-    grid_dependency_wait();
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        sts128(buffer + lane * 128 + (((chunk * 4 + i) ^ (lane & 7)) << 4),
+               make_uint4(pack2(v[8 * i], v[8 * i + 1], f16), pack2(v[8 * i + 2], v[8 * i + 3], f16),
+                          pack2(v[8 * i + 4], v[8 * i + 5], f16), pack2(v[8 * i + 6], v[8 * i + 7], f16)));
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ float4 lds_float4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+// Writes the staged rows to (row, col) of the output: by TMA where its rows are
+// whole 16 bytes (what lies outside is not written), otherwise element by element.
+__device__ __forceinline__ void write_staged(uint32_t buffer, const void *map, const TileArgs &a, int64_t row, int64_t col)
+{
     const int lane = threadIdx.x & 31;
-    const int64_t pieces = (a.inner + 255) / 256, n = a.rows * pieces;
-    for (int64_t w = blockIdx.x * 8ll + (threadIdx.x >> 5); w < n; w += gridDim.x * 8ll) {
-        const int64_t row = w / pieces, c0 = w % pieces * 256;
-        F8 g[1], u[1];
-        auto value = [&](int k, int64_t c) {
-            if (c >= a.inner)
-                return 0.f;
-            const float v = z[(row * 2 + k) * a.inner + c];
-            return a.bias ? v + load_param(a.bias, a.param_dtype, k * a.inner + c) : v;
-        };
-        for (int i = 0; i < 4; i++) {
-            const int64_t c = c0 + lane * 8 + 2 * i;
-            g[0].v[i] = make_float2(value(0, c), value(0, c + 1));
-            u[0].v[i] = make_float2(value(1, c), value(1, c + 1));
-            const float2 y = mul2(activation2<ACT>(g[0].v[i]), u[0].v[i]);
-            if (c < a.inner)
-                static_cast<T *>(a.y)[row * a.inner + c] = from_float<T>(y.x);
-            if (c + 1 < a.inner)
-                static_cast<T *>(a.y)[row * a.inner + c + 1] = from_float<T>(y.y);
+    if (a.tma_out) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row < a.rows && col < a.width) {
+            tma_store_2d(map, static_cast<int32_t>(col), static_cast<int32_t>(row), buffer);
+            bulk_commit();
         }
-        if (a.packed) {
-            const int col[1] = {lane * 8}, left = static_cast<int>(a.inner - c0);
-            for (int k = 0; k < 2; k++) {
-                uint8_t *to = a.packed + ((row * 2 + k) * a.inner + c0) / a.block * (a.block + 8);
-                if (a.code == 0)
-                    write_records<1, 0>(k ? u : g, col, left, to, a.block);
-                else if (a.code == 1)
-                    write_records<1, 1>(k ? u : g, col, left, to, a.block);
-                else
-                    write_records<1, 2>(k ? u : g, col, left, to, a.block);
-            }
-        }
+        return;
+    }
+    __syncwarp();
+    for (int r = 0; r < 32 && row + r < a.rows; r++)
+#pragma unroll
+        for (int c = lane; c < 64; c += 32)
+            if (col + c < a.width)
+                static_cast<uint16_t *>(a.out)[(row + r) * a.width + col + c] =
+                    static_cast<uint16_t>(lds16(buffer + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2));
+    __syncwarp();
+}
+
+// 32 accumulators of this thread's row, with the bias of column c on.
+__device__ __forceinline__ void load_z(uint32_t from, const TileArgs &a, int64_t bias_at, int64_t c, float (&z)[32])
+{
+    uint32_t r[32];
+    tmem_ld32(from, r);
+    tmem_ld_wait();
+    tmem_regs_ready(r);
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+        z[i] = __uint_as_float(r[i]);
+    if (a.bias) {
+        for (int i = 0; i < 32; i++)
+            if (c + i < a.width)
+                z[i] += load_param(a.bias, a.param_dtype, bias_at + c + i);
     }
 }
 
-template <typename T>
-cudaError_t gated(const GatedArgs &a, int sms, cudaStream_t stream)
+template <int CODE>
+__device__ __forceinline__ void encode_row32(const float (&z)[32], float inv, uint32_t to)
 {
-    const T *x = static_cast<const T *>(a.x), *w = static_cast<const T *>(a.weight);
-    float *z = static_cast<float *>(a.workspace);
-    int64_t M = a.rows, N = 2 * a.inner, K = a.hidden;
-    void *p[] = {&x, &w, &z, &M, &N, &K};
-    cudaError_t e = launch_kernel(reinterpret_cast<void *>(&taco_gated_product_kernel<T, float, false>), 4 * sms, 256, 0, stream, p);
-    if (e != cudaSuccess)
-        return e;
-    GatedArgs args = a;
-    void *q[] = {&args, &z};
-    return launch_kernel(a.activation == kSilu   ? reinterpret_cast<void *>(&taco_gated_finish_kernel<T, kSilu>)
-                         : a.activation == kGelu ? reinterpret_cast<void *>(&taco_gated_finish_kernel<T, kGelu>)
-                                                 : reinterpret_cast<void *>(&taco_gated_finish_kernel<T, kGeluTanh>),
-                         8 * sms, 256, 0, stream, q);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float *v = z + 8 * i;
+        const uint32_t lo = encode4_scaled(CODE, make_float2(v[0], v[1]), make_float2(v[2], v[3]), inv);
+        const uint32_t hi = encode4_scaled(CODE, make_float2(v[4], v[5]), make_float2(v[6], v[7]), inv);
+        sts64(to + 8 * i, inv == 0.f ? 0u : lo, inv == 0.f ? 0u : hi);
+    }
 }
 
-template <typename T>
-cudaError_t input_grad(const GatedInputGradArgs &a, int sms, cudaStream_t stream)
+// Records of 128 columns of one projection (k: 0 gate, 1 up) from column c on, 32
+// rows from `row` on; `from` the accumulator's first column.  The rows' record
+// bytes go through the buffer, `units` of eight bytes (an odd pitch of them), and
+// out in row order.
+__device__ __forceinline__ void write_tile_records(uint32_t from, uint32_t buffer, const TileArgs &a, int k, int64_t row, int64_t c)
 {
-    const T *dz = static_cast<const T *>(a.dz), *w = static_cast<const T *>(a.weight);
-    T *dx = static_cast<T *>(a.dx);
-    int64_t M = a.rows, N = a.hidden, K = 2 * a.inner;
-    void *p[] = {&dz, &w, &dx, &M, &N, &K};
-    return launch_kernel(reinterpret_cast<void *>(&taco_gated_product_kernel<T, T, true>), 4 * sms, 256, 0, stream, p);
+    const int lane = threadIdx.x & 31, shift = 31 - __clz(a.block);
+    const int cols = static_cast<int>(a.width - c < 128 ? a.width - c : 128);
+    uint32_t top[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        top[j] = 0;
+        if (32 * j < cols) {
+            float z[32];
+            load_z(from + 32 * j, a, k * a.width, c + 32 * j, z);
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                top[j] = max(top[j], abs_bits(z[i]));
+        }
+    }
+    if (a.block >= 64) {
+        top[0] = top[1] = max(top[0], top[1]);
+        top[2] = top[3] = max(top[2], top[3]);
+    }
+    if (a.block == 128)
+        top[0] = top[1] = top[2] = top[3] = max(top[0], top[2]);
+    const int units = 16 + (128 >> shift);
+    const uint32_t mine = buffer + lane * ((units | 1) * 8);
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (32 * j < cols) {
+            float z[32], inv;
+            load_z(from + 32 * j, a, k * a.width, c + 32 * j, z);
+            const float s = record_scale(top[j], a.code, &inv);
+            const uint32_t to = mine + 32 * j + (32 * j >> shift) * 8;
+            if (a.code == 0)
+                encode_row32<0>(z, inv, to);
+            else if (a.code == 1)
+                encode_row32<1>(z, inv, to);
+            else
+                encode_row32<2>(z, inv, to);
+            if ((32 * (j + 1) & (a.block - 1)) == 0)
+                sts64(to + 32, __float_as_uint(1.f), __float_as_uint(s));
+        }
+    __syncwarp();
+    const int64_t half = (a.width >> shift) * (a.block + 8);
+    uint8_t *out = a.packed + (row * 2 + k) * half + (c >> shift) * (a.block + 8);
+    const int have = (cols + (cols >> shift) * 8) / 8, rows = static_cast<int>(a.rows - row < 32 ? a.rows - row : 32);
+    for (int i = lane; i < rows * have; i += 32) {
+        const int r = i / have, u = i - r * have;
+        *reinterpret_cast<uint2 *>(out + r * 2 * half + u * 8) = lds64(buffer + r * ((units | 1) * 8) + u * 8);
+    }
+    __syncwarp();
 }
+
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_out, TileArgs a, Plan plan, uint32_t idesc, uint32_t *fault)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) Barriers bars;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t first_unit = blockIdx.x >> 1, step_units = gridDim.x >> 1;
+    auto bar = [](uint64_t &b) { return smem_addr(&b); };
+
+    grid_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; s++) {
+            mbar_init(bar(bars.full[s]), 1);
+            mbar_init(bar(bars.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(bar(bars.acc_full[b]), 1);
+            mbar_init(bar(bars.acc_empty[b]), 16);   // eight epilogue warps of each CTA
+        }
+        mbar_init(bar(bars.drained), 1);
+        fence_mbar_init();
+        prefetch_tmap(&map_a);
+        prefetch_tmap(&map_b);
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&bars.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before_sync();
+    cta_barrier();
+    cluster_barrier();
+    tc_fence_after_sync();
+    const uint32_t tmem = bars.tmem;
+    grid_dependency_wait();
+
+    if (warp == 0 && lane == 0) {
+        const uint32_t full0 = in_even_cta(bar(bars.full[0]));
+        int s = 0;
+        uint32_t phase = 0, used = 0;
+        bool ok = true;
+        for (int64_t u = first_unit; u < plan.units && ok; u += step_units) {
+            int m, n, first, count;
+            int64_t part;
+            plan.at(u, m, n, part, first, count);
+            const int row = m * kTileM + static_cast<int>(rank) * 128;
+            for (int k = first; k < first + count; k++) {
+                if (!mbar_wait_bounded_thread(bar(bars.empty[s]), phase ^ 1u, fault, kFaultGated)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = base + s * kStageBytes, full = full0 + s * 8;
+                if (rank == 0)   // both CTAs' bytes; those of the odd one may have come already
+                    mbar_arrive_expect_tx(bar(bars.full[s]), 2 * kStageBytes);
+                pair_load_2d(dst, &map_a, k * kStageK, row, full);
+                if (ACT == kInputGrad) {
+                    const int col = n * 256 + static_cast<int>(rank) * 128;
+                    pair_load_2d(dst + kOperandBytes, &map_b, col, k * kStageK, full);
+                    pair_load_2d(dst + kOperandBytes + kHalfBytes, &map_b, col + 64, k * kStageK, full);
+                } else {
+                    pair_load_2d(dst + kOperandBytes, &map_b, k * kStageK, n * 128 + (rank ? static_cast<int>(a.width) : 0), full);
+                }
+                used |= 1u << s;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // No commit of `empty` may arrive after this CTA is gone, nor a copy land, which the products have waited for: the
+        // last phase of every stage that was filled.  Once a wait has given up, nothing that is on its way takes as long as
+        // that wait did.
+        bool arrives = true;
+        for (int i = 0; i < kStages; i++)
+            if (used >> i & 1u)
+                arrives = arrives && mbar_wait_bounded_thread(bar(bars.empty[i]), i < s ? phase : phase ^ 1u, fault, kFaultGated);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        int s = 0;
+        uint32_t phase = 0, turn = 0;
+        bool ok = true;
+        for (int64_t u = first_unit; u < plan.units && ok; u += step_units, turn++) {
+            int m, n, first, count;
+            int64_t part;
+            plan.at(u, m, n, part, first, count);
+            const uint32_t b = turn & 1u;
+            if (turn >= 2 && !cluster_wait(bar(bars.acc_empty[b]), ((turn >> 1) - 1) & 1u, fault, kFaultGated)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            for (int k = 0; k < count; k++) {
+                if (!cluster_wait(bar(bars.full[s]), phase, fault, kFaultGated)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t sa = base + s * kStageBytes, sb = sa + kOperandBytes;
+#pragma unroll
+                for (int j = 0; j < kStageK / 16; j++)
+                    pair_mma(tmem + b * 256, sw128_kmajor_desc(sa + j * 32),
+                             ACT == kInputGrad ? mn_desc(sb + j * 2048, kHalfBytes) : sw128_kmajor_desc(sb + j * 32), idesc, k > 0 || j > 0);
+                pair_commit(bar(bars.empty[s]));
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (ok)
+                pair_commit(bar(bars.acc_full[b]));
+        }
+        if (!ok) {   // no product may read memory that the CTAs give up below
+            own_commit(bar(bars.drained));
+            mbar_wait_bounded_thread(bar(bars.drained), 0, fault, kFaultGated);
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t empty0 = in_even_cta(bar(bars.acc_empty[0]));
+        const uint32_t buffer = base + kStages * kStageBytes + (warp - 4) * kWarpBytes;
+        uint32_t turn = 0;
+        for (int64_t u = first_unit; u < plan.units; u += step_units, turn++) {
+            int m, n, first, count;
+            int64_t part;
+            plan.at(u, m, n, part, first, count);
+            const uint32_t b = turn & 1u;
+            if (!mbar_wait_bounded(bar(bars.acc_full[b]), (turn >> 1) & 1u, fault, kFaultGated))
+                break;
+            tc_fence_after_sync();
+            const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + b * 256;
+            const int row0 = static_cast<int>(rank) * 128 + quarter * 32;
+            const int64_t row = static_cast<int64_t>(m) * kTileM + row0;
+            bulk_wait_read<0>();   // (the lane that stored) the buffer's last tile is on its way
+            __syncwarp();
+            if (ACT == kInputGrad && part >= 0) {
+                // 32 columns at a time, turned so that eight lanes write 128 consecutive bytes
+                float *to = a.parts + (part * kTileM + row0) * 256 + half * 128;
+                for (int c = 0; c < 4; c++) {
+                    float z[32];
+                    load_z(acc + half * 128 + c * 32, a, 0, 0, z);
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        sts128(buffer + lane * 128 + ((i ^ (lane & 7)) << 4),
+                               make_uint4(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]), __float_as_uint(z[4 * i + 2]),
+                                          __float_as_uint(z[4 * i + 3])));
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 32; r += 4) {
+                        const int at = r + (lane >> 3), unit = lane & 7;
+                        *reinterpret_cast<float4 *>(to + at * 256 + c * 32 + unit * 4) =
+                            lds_float4(buffer + at * 128 + ((unit ^ (at & 7)) << 4));
+                    }
+                    __syncwarp();
+                }
+            } else if (ACT == kInputGrad) {
+                for (int c = 0; c < 2; c++) {
+                    const uint32_t place = buffer + c * 4096;
+                    for (int j = 0; j < 2; j++) {
+                        float z[32];
+                        load_z(acc + half * 128 + c * 64 + j * 32, a, 0, 0, z);
+                        stage_row32(place, lane, j, z, a.f16);
+                    }
+                    write_staged(place, &map_out, a, row, static_cast<int64_t>(n) * 256 + half * 128 + c * 64);
+                }
+            } else {
+                const int64_t c0 = static_cast<int64_t>(n) * 128;
+                for (int j = 0; j < 2; j++) {
+                    const int c = half * 64 + j * 32;
+                    float g[32], v[32];
+                    load_z(acc + c, a, 0, c0 + c, g);
+                    load_z(acc + 128 + c, a, a.width, c0 + c, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y = mul2(activation2<ACT == kInputGrad ? 0 : ACT>(make_float2(g[i], g[i + 1])), make_float2(v[i], v[i + 1]));
+                        v[i] = y.x;
+                        v[i + 1] = y.y;
+                    }
+                    stage_row32(buffer, lane, j, v, a.f16);
+                }
+                write_staged(buffer, &map_out, a, row, c0 + half * 64);
+                if (a.packed) {
+                    bulk_wait_read<0>();
+                    __syncwarp();
+                    write_tile_records(acc + half * 128, buffer, a, half, row, c0);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                cluster_arrive(empty0 + b * 8);
+        }
+        bulk_wait_all<0>();
+    }
+    tc_fence_before_sync();
+    cta_barrier();
+    cluster_barrier();
+    tc_fence_after_sync();
+    __syncwarp();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Adds the K ranges' sums of the last tiles in order and rounds them, two columns a thread.
+__global__ void __launch_bounds__(256) taco_gated_join_kernel(TileArgs a, Plan plan)
+{
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t n = static_cast<int64_t>(plan.tail) * kTileM * 256;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 2; i < n; i += 512ll * gridDim.x) {
+        int tm, tn;
+        plan.tile(plan.whole + i / (kTileM * 256), tm, tn);
+        const int64_t row = static_cast<int64_t>(tm) * kTileM + i / 256 % kTileM, col = static_cast<int64_t>(tn) * 256 + i % 256;
+        if (row >= a.rows || col >= a.width)
+            continue;
+        float2 v = *reinterpret_cast<const float2 *>(a.parts + i);
+        for (int s = 1; s < plan.splits; s++)
+            v = add2(v, *reinterpret_cast<const float2 *>(a.parts + s * n + i));
+        const uint32_t w = pack2(v.x, v.y, a.f16);
+        uint16_t *to = static_cast<uint16_t *>(a.out) + row * a.width + col;
+        to[0] = static_cast<uint16_t>(w);
+        if (col + 1 < a.width)
+            to[1] = static_cast<uint16_t>(w >> 16);
+    }
+}
+
+const void *kernel_of(int activation)
+{
+    return activation == kSilu       ? reinterpret_cast<void *>(&taco_gated_kernel<kSilu>)
+           : activation == kGelu     ? reinterpret_cast<void *>(&taco_gated_kernel<kGelu>)
+           : activation == kGeluTanh ? reinterpret_cast<void *>(&taco_gated_kernel<kGeluTanh>)
+                                     : reinterpret_cast<void *>(&taco_gated_kernel<kInputGrad>);
+}
+
+cudaError_t launch_pairs(const void *fn, int pairs, cudaStream_t stream, void **args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = TACO_PDL ? 1 : 0;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// Row tiles of a group: about 32 MB of A, a quarter of L2, and at least the rows of a square of 76 tiles.
+int group_of(int64_t tiles_m, int64_t K)
+{
+    return static_cast<int>(std::min<int64_t>(tiles_m, std::max<int64_t>(8, (32 << 20) / (kTileM * 2 * K))));
+}
+
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+constexpr uint32_t kDescF16 = mma_idesc_f16_f32(256, 256), kDescBf16 = mma_idesc_bf16_f32(256, 256);
 
 }  // namespace
 
-cudaError_t init_gated() { return cudaSuccess; }
+cudaError_t init_gated()
+{
+    cudaError_t e = cudaSuccess;
+    for (int act = kInputGrad; act <= kGeluTanh && e == cudaSuccess; act++)
+        e = cudaFuncSetAttribute(kernel_of(act), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    return e;
+}
 
 bool gated_in_range(int64_t rows, int64_t inner, int64_t hidden)
 {
-    // 32-bit coordinates, whole tiles past the end included
+    // 32-bit TMA coordinates, whole tiles and stages past the end included
     return rows <= INT32_MAX - 256 && inner <= INT32_MAX / 2 - 256 && hidden <= INT32_MAX - 256;
 }
 
-int64_t gated_workspace(int64_t rows, int64_t inner, int64_t) { return 8 * rows * inner; }
-
-int64_t gated_input_grad_workspace(int64_t, int64_t, int64_t) { return 0; }
-
-cudaError_t launch_gated(const GatedArgs &a, uint32_t *, int sms, cudaStream_t stream)
+// x and W in rows of whole 16 bytes where they have others.
+int64_t gated_workspace(int64_t rows, int64_t inner, int64_t hidden)
 {
-    return a.dtype == kTypeBf16 ? gated<__nv_bfloat16>(a, sms, stream) : gated<__half>(a, sms, stream);
+    return hidden % 8 ? 2 * (rows + 2 * inner) * up8(hidden) : 0;
 }
 
-cudaError_t launch_gated_input_grad(const GatedInputGradArgs &a, uint32_t *, int sms, cudaStream_t stream)
+cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStream_t stream)
 {
-    return a.dtype == kTypeBf16 ? input_grad<__nv_bfloat16>(a, sms, stream) : input_grad<__half>(a, sms, stream);
+    const int64_t pitch = up8(a.hidden);
+    const void *x = a.x, *w = a.weight;
+    cudaError_t e = cudaSuccess;
+    if (pitch != a.hidden) {
+        uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+        e = launch_widen_rows(a.x, a.rows, a.hidden, pitch, ws, sms, stream);
+        if (e == cudaSuccess)
+            e = launch_widen_rows(a.weight, 2 * a.inner, a.hidden, pitch, ws + 2 * a.rows * pitch, sms, stream);
+        x = ws;
+        w = ws + 2 * a.rows * pitch;
+    }
+    const CUtensorMapDataType type = a.dtype == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    alignas(64) CUtensorMap map_x, map_w, map_y = {};
+    const bool tma_out = a.inner % 8 == 0;
+    if (e == cudaSuccess)
+        e = encode_2d(&map_x, type, x, a.hidden, a.rows, 2 * pitch, kStageK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+        e = encode_2d(&map_w, type, w, a.hidden, 2 * a.inner, 2 * pitch, kStageK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess && tma_out)
+        e = encode_2d(&map_y, type, a.y, a.inner, a.rows, 2 * a.inner, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess)
+        return e;
+    Plan plan = {};
+    plan.tiles_m = static_cast<int>((a.rows + kTileM - 1) / kTileM);
+    plan.tiles_n = static_cast<int>((a.inner + 127) / 128);
+    plan.group_m = group_of(plan.tiles_m, a.hidden);
+    plan.stages_total = static_cast<int>((a.hidden + kStageK - 1) / kStageK);
+    plan.whole = plan.units = static_cast<int64_t>(plan.tiles_m) * plan.tiles_n;
+    plan.splits = 1;
+    TileArgs args{a.y, a.packed, a.bias, nullptr, a.rows, a.inner, a.param_dtype, a.block, a.code, a.dtype == kTypeF16, tma_out};
+    uint32_t idesc = a.dtype == kTypeF16 ? kDescF16 : kDescBf16;
+    void *p[] = {&map_x, &map_w, &map_y, &args, &plan, &idesc, &fault};
+    return launch_pairs(kernel_of(a.activation), static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
+}
+
+// Tiles of dx, how many at the end are cut into ranges of K, and into how many:
+// with few tiles each wave's pairs would otherwise wait for a few long sums.
+// The pairs of a GB300, not of the current device: the workspace query that shares
+// the plan looks at none.  With another count the plan is only less even.
+constexpr int64_t kPairs = 76;
+
+struct Split {
+    int64_t tiles, tail, splits;
+};
+
+static Split input_grad_split(int64_t rows, int64_t inner, int64_t hidden)
+{
+    Split s{((rows + kTileM - 1) / kTileM) * ((hidden + 255) / 256), 0, 1};
+    s.tail = s.tiles % kPairs;
+    if (s.tail > 0)
+        s.splits = std::max<int64_t>(1, std::min(kPairs / s.tail, 2 * inner / 512));
+    if (s.splits == 1)
+        s.tail = 0;
+    return s;
+}
+
+static int64_t input_grad_part_bytes(const Split &s) { return s.tail * s.splits * kTileM * 256 * 4; }
+
+// The K ranges' sums, then W in rows of whole 16 bytes where it has others.
+int64_t gated_input_grad_workspace(int64_t rows, int64_t inner, int64_t hidden)
+{
+    return input_grad_part_bytes(input_grad_split(rows, inner, hidden)) + (hidden % 8 ? 4 * inner * up8(hidden) : 0);
+}
+
+cudaError_t launch_gated_input_grad(const GatedInputGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream)
+{
+    const Split s = input_grad_split(a.rows, a.inner, a.hidden);
+    const int64_t pitch = up8(a.hidden), K = 2 * a.inner;
+    const void *w = a.weight;
+    cudaError_t e = cudaSuccess;
+    if (pitch != a.hidden) {
+        void *to = static_cast<uint8_t *>(a.workspace) + input_grad_part_bytes(s);
+        e = launch_widen_rows(a.weight, K, a.hidden, pitch, to, sms, stream);
+        w = to;
+    }
+    const CUtensorMapDataType type = a.dtype == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    alignas(64) CUtensorMap map_dz, map_w, map_dx = {};
+    const bool tma_out = a.hidden % 8 == 0;
+    if (e == cudaSuccess)
+        e = encode_2d(&map_dz, type, a.dz, K, a.rows, 2 * K, kStageK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+        e = encode_2d(&map_w, type, w, a.hidden, K, 2 * pitch, 64, kStageK, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess && tma_out)
+        e = encode_2d(&map_dx, type, a.dx, a.hidden, a.rows, 2 * a.hidden, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess)
+        return e;
+    Plan plan = {};
+    plan.tiles_m = static_cast<int>((a.rows + kTileM - 1) / kTileM);
+    plan.tiles_n = static_cast<int>((a.hidden + 255) / 256);
+    plan.group_m = group_of(plan.tiles_m, K);
+    plan.stages_total = static_cast<int>((K + kStageK - 1) / kStageK);
+    plan.tail = static_cast<int>(s.tail);
+    plan.splits = static_cast<int>(s.splits);
+    plan.whole = s.tiles - s.tail;
+    plan.units = plan.whole + s.tail * s.splits;
+    TileArgs args{a.dx, nullptr, nullptr, static_cast<float *>(a.workspace), a.rows, a.hidden, 0, 0, 0, a.dtype == kTypeF16, tma_out};
+    uint32_t idesc = (a.dtype == kTypeF16 ? kDescF16 : kDescBf16) | (1u << 16);   // B N-major
+    void *p[] = {&map_dz, &map_w, &map_dx, &args, &plan, &idesc, &fault};
+    e = launch_pairs(kernel_of(kInputGrad), static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
+    if (e == cudaSuccess && plan.tail > 0) {
+        void *q[] = {&args, &plan};
+        e = launch_kernel(reinterpret_cast<void *>(&taco_gated_join_kernel),
+                          static_cast<int>(std::min<int64_t>(s.tail * 128, 8ll * sms)), 256, 0, stream, q);
+    }
+    return e;
 }
 
 }  // namespace taco

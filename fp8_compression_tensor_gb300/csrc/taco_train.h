@@ -160,6 +160,9 @@ int64_t weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden);
 bool weight_grad_in_range(int64_t rows, int64_t out, int64_t hidden);
 cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
 
+// Rows of `out` 16-bit elements copied `width` (a multiple of 8) apart, zeros behind each.
+cudaError_t launch_widen_rows(const void *from, int64_t rows, int64_t out, int64_t width, void *to, int sms, cudaStream_t stream);
+
 // out[c] = sum over p < nparts of parts[p][c] in a fixed order; zeros for nparts = 0.  parts holds two
 // such arrays ([2][nparts][n]) where out2 takes the second one's sums; either output may be null.
 cudaError_t launch_column_sums(const float *parts, int nparts, int64_t n, void *out, void *out2, int dtype,

@@ -36,7 +36,7 @@
 
 #include "taco_host.h"
 #include "taco_kernels.h"
-#include "taco_tcgen05.cuh"
+#include "taco_pair.cuh"
 #include "taco_train.cuh"
 
 namespace taco {
@@ -96,10 +96,10 @@ __global__ void __launch_bounds__(256) taco_weight_grad_empty_kernel(WeightGradA
     }
 }
 
-// dY with rows of a multiple of 8 elements: TMA reads rows of whole 16 bytes, so
-// where `out` is no multiple of 8 the rows are first copied `width` elements
-// apart (zeros behind each), eight elements a thread.
-__global__ void __launch_bounds__(256) taco_weight_grad_widen_kernel(const uint16_t *dy, int64_t rows, int64_t out, int64_t width, uint4 *to)
+// Rows of a multiple of 8 elements: TMA reads rows of whole 16 bytes, so where
+// `out` is no multiple of 8 the rows are first copied `width` elements apart
+// (zeros behind each), eight elements a thread.
+__global__ void __launch_bounds__(256) taco_widen_rows_kernel(const uint16_t *dy, int64_t rows, int64_t out, int64_t width, uint4 *to)
 {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -146,66 +146,6 @@ struct WgBarriers {
     uint32_t tmem;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// The even CTA's address of this CTA's shared-memory address.
-__device__ __forceinline__ uint32_t in_even_cta(uint32_t addr)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-    return r;
-}
-
-// An arrival from either CTA.  What it reports lies in the reporting CTA's own
-// shared and tensor memory and is read by the tensor core, for which the fences
-// before it (fence.proxy.async, tcgen05.fence) order the accesses; a release at
-// cluster scope would wait for all of the thread's memory operations besides and
-// took 8192 x 16384 x 4096 from 1.95 to 2.78 ms when it was tried.
-__device__ __forceinline__ void cluster_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool cluster_try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(TACO_WAIT_HINT_NS)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait for a barrier that the other CTA's threads arrive on too.  The
-// timer is read only after a first miss: the read alone costs more than a
-// stage's products.
-__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, uint32_t *fault)
-{
-    if (cluster_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = global_timer_ns();
-    while (!cluster_try_wait(bar, parity)) {
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(fault, kFaultWeightGrad);
-            return false;
-        }
-    }
-    return true;
-}
-
 // Barrier of the eight epilogue warps: whether `ok` holds for all of them.
 __device__ __forceinline__ bool epilogue_agrees(bool ok)
 {
@@ -217,56 +157,6 @@ __device__ __forceinline__ bool epilogue_agrees(bool ok)
         : "r"(static_cast<uint32_t>(ok))
         : "memory");
     return all != 0;
-}
-
-// MN-major operand in the 128-byte swizzled layout: rows of 64 MN-elements,
-// 8-row groups 1024 bytes apart, blocks of 64 MN-elements kHalfBytes apart.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t addr)
-{
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((kHalfBytes >> 4) & 0x3FFF) << 16;
-    d |= static_cast<uint64_t>((1024u >> 4) & 0x3FFFu) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
-}
-
-__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"(accumulate)
-        : "memory");
-}
-
-// One arrival on the barrier at this offset in both CTAs once the pair's products so far are done.
-__device__ __forceinline__ void pair_commit(uint32_t bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
-// The same in this CTA alone, for a barrier that only this thread waits for.
-__device__ __forceinline__ void own_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// 16 consecutive tensor-memory columns of this thread's lane, complete on return.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
 }
 
 // Two codes (low 16 bits of `pair`) times f, rounded to bf16 (exact for a power of two).
@@ -485,14 +375,14 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                 plan.at(u, m0, n0, part, first, count);
                 for (int k = 0; k < count && ok; chunk++) {
                     const int b = static_cast<int>(chunk & 1);
-                    if (chunk >= 2 && !cluster_wait(bar(bars.acc_empty[b]), ((chunk >> 1) - 1) & 1u, fault)) {
+                    if (chunk >= 2 && !cluster_wait(bar(bars.acc_empty[b]), ((chunk >> 1) - 1) & 1u, fault, kFaultWeightGrad)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const int end = min(count, k + kChunkRows / kStageRows);
                     for (const int begin = k; k < end; k++) {
-                        if (!cluster_wait(bar(bars.full[s]), phase, fault)) {
+                        if (!cluster_wait(bar(bars.full[s]), phase, fault, kFaultWeightGrad)) {
                             ok = false;
                             break;
                         }
@@ -500,7 +390,8 @@ taco_weight_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid
                         const uint32_t sa = base + s * 2 * kOperandBytes;
 #pragma unroll
                         for (int j = 0; j < kStageRows / 16; j++)
-                            pair_mma(tmem + b * kPairN, mn_desc(sa + j * 2048), mn_desc(sa + kOperandBytes + j * 2048),
+                            pair_mma(tmem + b * kPairN, mn_desc(sa + j * 2048, kHalfBytes),
+                                     mn_desc(sa + kOperandBytes + j * 2048, kHalfBytes), kIdesc,
                                      k > begin || j > 0);
                         pair_commit(bar(bars.empty[s]));
                         if (++s == kStages) {
@@ -766,23 +657,6 @@ cudaError_t launch_pairs(const void *fn, int pairs, cudaStream_t stream, void **
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-// Tensor map of [rows, width] elements `pitch` bytes apart, boxes {box_x, box_y}; what lies outside reads zeros.
-cudaError_t encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t width, int64_t rows, int64_t pitch,
-                      int box_x, int box_y, CUtensorMapSwizzle swizzle)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    const cudaError_t e = tensor_map_encoder(&encode);
-    if (e != cudaSuccess)
-        return e;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y)}, elem_strides[2] = {1, 1};
-    return encode(map, type, 2, const_cast<void *>(base), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 cudaError_t init_weight_grad()
@@ -830,6 +704,13 @@ bool weight_grad_in_range(int64_t rows, int64_t out, int64_t hidden)
     return rows <= INT32_MAX - 64 && out <= INT32_MAX - 256 && hidden <= INT32_MAX / 2;
 }
 
+cudaError_t launch_widen_rows(const void *from, int64_t rows, int64_t out, int64_t width, void *to, int sms, cudaStream_t stream)
+{
+    void *p[] = {&from, &rows, &out, &width, &to};
+    return launch_kernel(reinterpret_cast<void *>(&taco_widen_rows_kernel),
+                         static_cast<int>(std::min<int64_t>((rows * width + 2047) / 2048, 8ll * sms)), 256, 0, stream, p);
+}
+
 cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream)
 {
     WeightGradArgs args = a;
@@ -843,11 +724,7 @@ cudaError_t launch_weight_grad(const WeightGradArgs &a, uint32_t *fault, int sms
     const void *dy = a.dy;
     if (width != a.out) {
         void *to = reinterpret_cast<uint8_t *>(a.parts) + weight_grad_part_bytes(w);
-        int64_t rows = a.rows, out = a.out;
-        void *p[] = {&dy, &rows, &out, &width, &to};
-        const cudaError_t e = launch_kernel(reinterpret_cast<void *>(&taco_weight_grad_widen_kernel),
-                                            static_cast<int>(std::min<int64_t>((rows * width + 2047) / 2048, 8ll * sms)), 256, 0,
-                                            stream, p);
+        const cudaError_t e = launch_widen_rows(dy, a.rows, a.out, width, to, sms, stream);
         if (e != cudaSuccess)
             return e;
         dy = to;
