@@ -493,7 +493,7 @@ cudaError_t init_gated()
     cudaError_t e = cudaSuccess;
     for (int act = kInputGrad; act <= kGeluTanh && e == cudaSuccess; act++)
         e = cudaFuncSetAttribute(kernel_of(act), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    return e;
+    return e == cudaSuccess ? init_gated_serve() : e;
 }
 
 bool gated_in_range(int64_t rows, int64_t inner, int64_t hidden)
@@ -521,6 +521,8 @@ cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStrea
         x = ws;
         w = ws + 2 * a.rows * pitch;
     }
+    if (e == cudaSuccess && !a.packed && gated_serves(a.rows))
+        return launch_gated_serve(a, x, w, pitch, fault, sms, stream);
     const CUtensorMapDataType type = a.dtype == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     alignas(64) CUtensorMap map_x, map_w, map_y = {};
     const bool tma_out = a.inner % 8 == 0;
