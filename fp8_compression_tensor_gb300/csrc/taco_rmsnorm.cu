@@ -5,7 +5,7 @@
 //   rstd = 1 / sqrt(sum h^2 / C + eps),  xhat = h rstd,  y = xhat weight,
 // y as a tensor or as records, and optionally the records of xhat
 // (taco_train.cuh).  Sums are binary32.
-#include "taco_norm.cuh"
+#include "taco_rms.cuh"
 
 namespace taco {
 namespace {
@@ -133,9 +133,202 @@ __global__ void __launch_bounds__(kWideThreads) taco_rms_wide_kernel(RmsArgs a)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Rows in registers
+// ---------------------------------------------------------------------------
+
+// The layer norm's arrangement: a row's vectors over a group of `warps` warps,
+// vector j (of NV) of warp w, lane l being (w NV + j) 32 + l, the CTA's groups on
+// rows of their own, rows on their way to shared memory `stages` ahead by
+// cp.async, each piece copied by the thread that reads it.  One row sum, one
+// barrier.
+// STAGED: the weight lies in shared memory, where a CTA has several rows to read
+// it for.  ODD: rows start anywhere (taco_rms.cuh).  FULL: every lane's every
+// vector lies inside the row.
+constexpr int kRmsThreads = 768;
+
+template <typename T, int NV, bool STAGED, bool ODD, bool FULL>
+__global__ void __launch_bounds__(kRmsThreads, 1) taco_rms_kernel(RmsArgs a, int warps, int groups, int stages)
+{
+    extern __shared__ __align__(16) uint8_t dynamic[];   // weight (STAGED), then the copies
+    __shared__ float sums[2][32];
+    grid_launch_dependents();
+    constexpr int kUnits = sizeof(T) / 2;                 // 16-byte units of eight elements
+    const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
+    const int C = static_cast<int>(a.hidden), unit = blockDim.x * 16, vectors = row_vectors(C);
+    const int shift = ODD ? static_cast<int>(blockIdx.x * a.hidden & 7) : 0;
+    float *sparam = reinterpret_cast<float *>(dynamic);
+    const uint8_t *ring = dynamic + (STAGED ? 32 * vectors : 0) + threadIdx.x * 16;
+    const uint32_t ring_at = smem_addr(ring);
+    const int row_units = (a.residual ? 2 : 1) * NV * kUnits;
+    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
+    const int v0 = warp * NV * 32 + lane;
+    int col[NV];
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+        col[j] = (v0 + 32 * j) * 8 - shift;
+    const int64_t first = blockIdx.x + static_cast<int64_t>(gridDim.x) * group, step = static_cast<int64_t>(gridDim.x) * groups;
+    if (warp == 0 && lane < 2 && !ODD && first + lane * step < a.rows) {
+        // the group's first rows on their way to L2 while the kernel before still runs
+        bulk_prefetch_l2(x + (first + lane * step) * C, C * static_cast<int>(sizeof(T)));
+        if (res)
+            bulk_prefetch_l2(res + (first + lane * step) * C, C * static_cast<int>(sizeof(T)));
+    }
+    grid_dependency_wait();
+    const int64_t end = a.rows * a.hidden * static_cast<int>(sizeof(T));   // of the tensors, in bytes
+    auto copy_row = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            uint32_t to = ring_at + static_cast<uint32_t>(stage * row_units * unit);
+            auto piece = [&](const T *src) {
+#pragma unroll
+                for (int j = 0; j < NV; j++)
+#pragma unroll
+                    for (int k = 0; k < kUnits; k++, to += unit)
+                        if (FULL || col[j] < C) {
+                            const T *from = src + row * C + col[j] + 8 / kUnits * k;
+                            if (ODD) {
+                                // the tensor's last vector may end behind it
+                                const int64_t left = end - (row * C + col[j]) * static_cast<int>(sizeof(T)) - 16 * k;
+                                copy16_upto<T>(to, left > 0 ? from : src, left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0);
+                            } else {
+                                copy16<T>(to, from);
+                            }
+                        }
+            };
+            piece(x);
+            if (res)
+                piece(res);
+        }
+        copies_issued();
+    };
+    for (int i = 0; i < stages - 1; i++)
+        copy_row(first + i * step, i);
+    if (STAGED) {
+        stage_shifted<ODD>(sparam, a.weight, a.param_dtype, vectors, shift, C, 1.f);
+        __syncthreads();
+    }
+    auto weight = [&](int j) {
+        if (STAGED)
+            return load_shifted(sparam, v0 + 32 * j, vectors);
+        return ODD ? load_param_edge(a.weight, a.param_dtype, col[j], C, 1.f) : load_param_f8(a.weight, a.param_dtype, col[j]);
+    };
+    const float fc = static_cast<float>(C);
+    int stage = 0, fill = stages - 1;
+    uint32_t side = 0;
+    for (int64_t row = first; row < a.rows; row += step, side ^= 1u) {
+        copy_row(row + (stages - 1) * step, fill);
+        fill = fill + 1 == stages ? 0 : fill + 1;
+        copies_landed(stages - 1);
+        const uint8_t *mine = ring + static_cast<size_t>(stage) * row_units * unit;
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        F8 h[NV];
+        float2 squares = both(0.f);
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            if (FULL || col[j] < C) {
+                Raw8<T> v;
+#pragma unroll
+                for (int k = 0; k < kUnits; k++)
+                    v.v[k] = *reinterpret_cast<const uint4 *>(mine + (j * kUnits + k) * unit);
+                h[j] = unpack(v);
+                if (res) {
+#pragma unroll
+                    for (int k = 0; k < kUnits; k++)
+                        v.v[k] = *reinterpret_cast<const uint4 *>(mine + ((NV + j) * kUnits + k) * unit);
+                    const F8 r = unpack(v);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        h[j].v[i] = add2(h[j].v[i], r.v[i]);
+                    store_vector<T, ODD>(static_cast<T *>(a.summed) + row * C, h[j], col[j], C);
+                    h[j] = unpack(pack<T>(h[j]));
+                }
+                if (ODD && at_edge(col[j], C))
+                    mask_edge(h[j], col[j], C);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    squares = fma2(h[j].v[i], h[j].v[i], squares);
+            }
+        // `sums` alternates between two sets, so a set is written again only behind the next row's barrier
+        const float sq = group_sum(warp_sum(squares.x + squares.y), sums[side] + group * warps, group, warp, warps);
+        const float rstd = inv_sqrt(sq / fc + a.eps);
+        if (warp == 0 && lane == 0)
+            a.rstd[row] = rstd;
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            if (FULL || col[j] < C) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    h[j].v[i] = mul2(h[j].v[i], both(rstd));
+            }
+        if (!ODD && a.packed)
+            write_records_of<NV>(h, col, C, a.packed + row * (C / a.block) * (a.block + 8), a.block, a.code);
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            if (FULL || col[j] < C) {
+                if (STAGED || a.weight) {
+                    const F8 w = weight(j);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        h[j].v[i] = mul2(h[j].v[i], w.v[i]);
+                }
+                if (ODD || a.y)
+                    store_vector<T, ODD>(static_cast<T *>(a.y) + row * C, h[j], col[j], C);
+            }
+        if (!ODD && a.packed_y)
+            write_records_of<NV>(h, col, C, a.packed_y + row * (C / a.block) * (a.block + 8), a.block, a.code);
+    }
+}
+
+template <typename T, bool STAGED>
+const void *rms_kernel(int nv, bool odd, bool full)
+{
+    if (odd)
+        return nv == 1   ? reinterpret_cast<void *>(&taco_rms_kernel<T, 1, STAGED, true, false>)
+               : nv == 2 ? reinterpret_cast<void *>(&taco_rms_kernel<T, 2, STAGED, true, false>)
+                         : reinterpret_cast<void *>(&taco_rms_kernel<T, 4, STAGED, true, false>);
+    return nv == 1   ? reinterpret_cast<void *>(&taco_rms_kernel<T, 1, STAGED, false, false>)
+           : nv == 2 ? reinterpret_cast<void *>(&taco_rms_kernel<T, 2, STAGED, false, false>)
+           : full    ? reinterpret_cast<void *>(&taco_rms_kernel<T, 4, STAGED, false, true>)
+                     : reinterpret_cast<void *>(&taco_rms_kernel<T, 4, STAGED, false, false>);
+}
+
+template <typename T>
+const void *rms_kernel(int nv, bool staged, bool odd, bool full)
+{
+    return staged ? rms_kernel<T, true>(nv, odd, full) : rms_kernel<T, false>(nv, odd, full);
+}
+
+// Vectors that a CTA's warps hold, four a lane.
+constexpr int kRmsVectors = kRmsThreads * 4;
+
+template <typename T>
+bool rms_registers(const RmsArgs &a, int sms, cudaStream_t stream, cudaError_t *result)
+{
+    if (row_vectors(a.hidden) > kRmsVectors)
+        return false;
+    RmsArgs args = a;
+    const int vectors = row_vectors(a.hidden), nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;
+    int warps = (vectors + 32 * nv - 1) / (32 * nv);
+    int groups = row_groups(a.rows, warps, kRmsThreads, sms);
+    const size_t place = static_cast<size_t>(a.residual ? 2 : 1) * nv * warps * 256 * sizeof(T), params = 32 * static_cast<size_t>(vectors);
+    while (groups > 1 && params + groups * place > max_shared<T>(196))
+        groups--;
+    const size_t stage = groups * place;
+    const int64_t ctas = (a.rows + groups - 1) / groups;
+    const bool staged = ctas > sms && a.weight && params + stage <= kMaxShared;
+    int stages = ring_stages(staged ? params : 0, stage, max_shared<T>(196));
+    void *p[] = {&args, &warps, &groups, &stages};
+    *result = launch_kernel(rms_kernel<T>(nv, staged, a.hidden % 8 != 0, a.hidden == warps * nv * 256), shifted_grid(ctas, groups, a.hidden % 8 != 0, sms),
+                            warps * groups * 32, (staged ? params : 0) + stages * stage, stream, p);
+    return true;
+}
+
 template <typename T>
 cudaError_t rms_any(const RmsArgs &a, int sms, cudaStream_t stream)
 {
+    cudaError_t result;
+    if (rms_registers<T>(a, sms, stream, &result))
+        return result;
     RmsArgs args = a;
     void *p[] = {&args};
     if (a.hidden % 8 == 0)
@@ -143,9 +336,28 @@ cudaError_t rms_any(const RmsArgs &a, int sms, cudaStream_t stream)
     return launch_kernel(reinterpret_cast<void *>(&taco_rms_any_kernel<T>), row_grid(a.rows, sms, 8), kRowThreads, 0, stream, p);
 }
 
+template <typename T>
+cudaError_t init_rms_type()
+{
+    for (int nv = 1; nv <= 4; nv *= 2)
+        for (int i = 0; i < 8; i++) {
+            const cudaError_t e = cudaFuncSetAttribute(rms_kernel<T>(nv, i & 1, i & 2, i & 4), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(kMaxShared));
+            if (e != cudaSuccess)
+                return e;
+        }
+    return cudaSuccess;
+}
+
 }  // namespace
 
-cudaError_t init_rms() { return cudaSuccess; }
+cudaError_t init_rms()
+{
+    cudaError_t e = init_rms_type<__nv_bfloat16>();
+    if (e == cudaSuccess)
+        e = init_rms_type<__half>();
+    return e == cudaSuccess ? init_rms_type<float>() : e;
+}
 
 cudaError_t launch_rms(int dtype, const RmsArgs &a, int sms, cudaStream_t stream)
 {
