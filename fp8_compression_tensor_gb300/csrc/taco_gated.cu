@@ -142,21 +142,49 @@ __device__ __forceinline__ void write_staged(uint32_t buffer, const void *map, c
     __syncwarp();
 }
 
-// 32 accumulators of this thread's row, with the bias of column c on.
-__device__ __forceinline__ void load_z(uint32_t from, const TileArgs &a, int64_t bias_at, int64_t c, float (&z)[32])
+// The bias of a tile's 128 gate and 128 up columns from c on, as binary32 in the
+// warp's buffer behind what it writes (zeros outside).  It is fetched ahead of the
+// accumulator's wait: loaded a column a lane where it is added, 333 x 1000 x 2048 with
+// records took 17 us.
+constexpr int kBiasAt = 6144;
+
+__device__ __forceinline__ void stage_bias(uint32_t buffer, const TileArgs &a, int64_t c)
 {
-    uint32_t r[32];
-    tmem_ld32(from, r);
-    tmem_ld_wait();
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int64_t col = c + 32 * (i & 3) + lane;
+        const float v = col < a.width ? load_param(a.bias, a.param_dtype, (i >> 2) * a.width + col) : 0.f;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(buffer + kBiasAt + (32 * i + lane) * 4), "f"(v) : "memory");
+    }
+    __syncwarp();
+}
+
+// 32 accumulators, as loaded, of this thread's row, and the bias of column `at` of the tile's 256 on.
+__device__ __forceinline__ void to_z(uint32_t (&r)[32], const TileArgs &a, uint32_t buffer, int at, float (&z)[32])
+{
     tmem_regs_ready(r);
 #pragma unroll
     for (int i = 0; i < 32; i++)
         z[i] = __uint_as_float(r[i]);
     if (a.bias) {
-        for (int i = 0; i < 32; i++)
-            if (c + i < a.width)
-                z[i] += load_param(a.bias, a.param_dtype, bias_at + c + i);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 v = lds_float4(buffer + kBiasAt + (at + i) * 4);
+            z[i] += v.x;
+            z[i + 1] += v.y;
+            z[i + 2] += v.z;
+            z[i + 3] += v.w;
+        }
     }
+}
+
+__device__ __forceinline__ void load_z(uint32_t acc, const TileArgs &a, uint32_t buffer, int at, float (&z)[32])
+{
+    uint32_t r[32];
+    tmem_ld32(acc + at, r);
+    tmem_ld_wait();
+    to_z(r, a, buffer, at, z);
 }
 
 template <int CODE>
@@ -172,56 +200,55 @@ __device__ __forceinline__ void encode_row32(const float (&z)[32], float inv, ui
 }
 
 // Records of 128 columns of one projection (k: 0 gate, 1 up) from column c on, 32
-// rows from `row` on; `from` the accumulator's first column.  The rows' record
-// bytes go through the buffer, `units` of eight bytes (an odd pitch of them), and
-// out in row order.
-__device__ __forceinline__ void write_tile_records(uint32_t from, uint32_t buffer, const TileArgs &a, int k, int64_t row, int64_t c)
+// rows from `row` on.  A block's accumulators are read twice, for its maximum and
+// for its codes.  The rows' record bytes go through the buffer, an odd number of
+// eight bytes apart, and out in row order.
+__device__ __forceinline__ void write_tile_records(uint32_t acc, uint32_t buffer, const TileArgs &a, int k, int64_t row, int64_t c)
 {
-    const int lane = threadIdx.x & 31, shift = 31 - __clz(a.block);
+    const int lane = threadIdx.x & 31, shift = 31 - __clz(a.block), block = a.block;
     const int cols = static_cast<int>(a.width - c < 128 ? a.width - c : 128);
-    uint32_t top[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        top[j] = 0;
-        if (32 * j < cols) {
-            float z[32];
-            load_z(from + 32 * j, a, k * a.width, c + 32 * j, z);
+    const uint32_t pitch = (16 + (128 >> shift) | 1) * 8;
+    uint32_t to = buffer + lane * pitch;
+#pragma unroll 1
+    for (int b = 0; b < cols; b += block) {
+        uint32_t top = 0;
+        float z[32], inv;
+#pragma unroll 1
+        for (int j = b; j < b + block; j += 32) {
+            load_z(acc, a, buffer, k * 128 + j, z);
 #pragma unroll
             for (int i = 0; i < 32; i++)
-                top[j] = max(top[j], abs_bits(z[i]));
+                top = max(top, abs_bits(z[i]));
         }
-    }
-    if (a.block >= 64) {
-        top[0] = top[1] = max(top[0], top[1]);
-        top[2] = top[3] = max(top[2], top[3]);
-    }
-    if (a.block == 128)
-        top[0] = top[1] = top[2] = top[3] = max(top[0], top[2]);
-    const int units = 16 + (128 >> shift);
-    const uint32_t mine = buffer + lane * ((units | 1) * 8);
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-        if (32 * j < cols) {
-            float z[32], inv;
-            load_z(from + 32 * j, a, k * a.width, c + 32 * j, z);
-            const float s = record_scale(top[j], a.code, &inv);
-            const uint32_t to = mine + 32 * j + (32 * j >> shift) * 8;
+        const float s = record_scale(top, a.code, &inv);
+#pragma unroll 1
+        for (int j = b; j < b + block; j += 32, to += 32) {
+            if (block > 32)
+                load_z(acc, a, buffer, k * 128 + j, z);
             if (a.code == 0)
                 encode_row32<0>(z, inv, to);
             else if (a.code == 1)
                 encode_row32<1>(z, inv, to);
             else
                 encode_row32<2>(z, inv, to);
-            if ((32 * (j + 1) & (a.block - 1)) == 0)
-                sts64(to + 32, __float_as_uint(1.f), __float_as_uint(s));
         }
+        sts64(to, __float_as_uint(1.f), __float_as_uint(s));
+        to += 8;
+    }
     __syncwarp();
-    const int64_t half = (a.width >> shift) * (a.block + 8);
-    uint8_t *out = a.packed + (row * 2 + k) * half + (c >> shift) * (a.block + 8);
+    const int64_t half = (a.width >> shift) * (block + 8);
+    uint8_t *out = a.packed + (row * 2 + k) * half + (c >> shift) * (block + 8);
     const int have = (cols + (cols >> shift) * 8) / 8, rows = static_cast<int>(a.rows - row < 32 ? a.rows - row : 32);
-    for (int i = lane; i < rows * have; i += 32) {
-        const int r = i / have, u = i - r * have;
-        *reinterpret_cast<uint2 *>(out + r * 2 * half + u * 8) = lds64(buffer + r * ((units | 1) * 8) + u * 8);
+    const int step_r = 32 / have, step_u = 32 - step_r * have;
+    int r = lane / have, u = lane - r * have;
+    while (r < rows) {
+        *reinterpret_cast<uint2 *>(out + r * 2 * half + u * 8) = lds64(buffer + r * pitch + u * 8);
+        r += step_r;
+        u += step_u;
+        if (u >= have) {
+            u -= have;
+            r++;
+        }
     }
     __syncwarp();
 }
@@ -354,6 +381,8 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             int64_t part;
             plan.at(u, m, n, part, first, count);
             const uint32_t b = turn & 1u;
+            if (ACT != kInputGrad && a.bias)
+                stage_bias(buffer, a, static_cast<int64_t>(n) * 128);
             if (!mbar_wait_bounded(bar(bars.acc_full[b]), (turn >> 1) & 1u, fault, kFaultGated))
                 break;
             tc_fence_after_sync();
@@ -367,7 +396,7 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 float *to = a.parts + (part * kTileM + row0) * 256 + half * 128;
                 for (int c = 0; c < 4; c++) {
                     float z[32];
-                    load_z(acc + half * 128 + c * 32, a, 0, 0, z);
+                    load_z(acc, a, buffer, half * 128 + c * 32, z);
 #pragma unroll
                     for (int i = 0; i < 8; i++)
                         sts128(buffer + lane * 128 + ((i ^ (lane & 7)) << 4),
@@ -387,18 +416,23 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     const uint32_t place = buffer + c * 4096;
                     for (int j = 0; j < 2; j++) {
                         float z[32];
-                        load_z(acc + half * 128 + c * 64 + j * 32, a, 0, 0, z);
+                        load_z(acc, a, buffer, half * 128 + c * 64 + j * 32, z);
                         stage_row32(place, lane, j, z, a.f16);
                     }
                     write_staged(place, &map_out, a, row, static_cast<int64_t>(n) * 256 + half * 128 + c * 64);
                 }
             } else {
                 const int64_t c0 = static_cast<int64_t>(n) * 128;
+#pragma unroll 1
                 for (int j = 0; j < 2; j++) {
                     const int c = half * 64 + j * 32;
+                    uint32_t rg[32], ru[32];
+                    tmem_ld32(acc + c, rg);
+                    tmem_ld32(acc + 128 + c, ru);
+                    tmem_ld_wait();
                     float g[32], v[32];
-                    load_z(acc + c, a, 0, c0 + c, g);
-                    load_z(acc + 128 + c, a, a.width, c0 + c, v);
+                    to_z(rg, a, buffer, c, g);
+                    to_z(ru, a, buffer, 128 + c, v);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         const float2 y = mul2(activation2<ACT == kInputGrad ? 0 : ACT>(make_float2(g[i], g[i + 1])), make_float2(v[i], v[i + 1]));
@@ -411,7 +445,7 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 if (a.packed) {
                     bulk_wait_read<0>();
                     __syncwarp();
-                    write_tile_records(acc + half * 128, buffer, a, half, row, c0);
+                    write_tile_records(acc, buffer, a, half, row, c0);
                 }
             }
             tc_fence_before_sync();
@@ -547,8 +581,15 @@ cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStrea
     return launch_pairs(kernel_of(a.activation), static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
 }
 
-// Tiles of dx, how many at the end are cut into ranges of K, and into how many:
-// with few tiles each wave's pairs would otherwise wait for a few long sums.
+// Tiles of dx, how many at the end are cut into ranges of K, and into how many.
+// 76 pairs take the tiles in waves; those of the last wave may be cut so that its
+// pairs finish together.  In units of 64 along K (0.27 us a tile) a cut costs what
+// its sums take to be written and read again (512 KB a range, 0.2) and the kernel
+// that joins them (11): taken where that leaves less than 85%.  257 x 1024 x 2752
+// (8 tiles) takes 16.0 us in nine ranges and 30.3 whole, 1000 x 2048 x 8192 (32
+// tiles) 77 in two and 99 whole; 8192 x 4096 x 16384 (56 tiles in the last wave of
+// 7) and 640 x 5120 x 13824 (60 tiles) would take 1411 and 154 cut, 1416 and 146
+// whole.
 // The pairs of a GB300, not of the current device: the workspace query that shares
 // the plan looks at none.  With another count the plan is only less even.
 constexpr int64_t kPairs = 76;
@@ -557,18 +598,25 @@ struct Split {
     int64_t tiles, tail, splits;
 };
 
-static Split input_grad_split(int64_t rows, int64_t inner, int64_t hidden)
+Split input_grad_split(int64_t rows, int64_t inner, int64_t hidden)
 {
+    const int64_t steps = (2 * inner + kStageK - 1) / kStageK;
     Split s{((rows + kTileM - 1) / kTileM) * ((hidden + 255) / 256), 0, 1};
     s.tail = s.tiles % kPairs;
-    if (s.tail > 0)
-        s.splits = std::max<int64_t>(1, std::min(kPairs / s.tail, 2 * inner / 512));
+    int64_t best = 17 * steps;   // twentieths
+    for (int64_t n = 2; s.tail > 0 && n <= std::min(std::max<int64_t>(8, kPairs / s.tail), steps / 8); n++) {
+        const int64_t time = 20 * ((s.tail * n + kPairs - 1) / kPairs * ((steps + n - 1) / n) + 11) + 4 * s.tail * n;
+        if (time < best) {
+            best = time;
+            s.splits = n;
+        }
+    }
     if (s.splits == 1)
         s.tail = 0;
     return s;
 }
 
-static int64_t input_grad_part_bytes(const Split &s) { return s.tail * s.splits * kTileM * 256 * 4; }
+int64_t input_grad_part_bytes(const Split &s) { return s.tail * s.splits * kTileM * 256 * 4; }
 
 // The K ranges' sums, then W in rows of whole 16 bytes where it has others.
 int64_t gated_input_grad_workspace(int64_t rows, int64_t inner, int64_t hidden)

@@ -19,9 +19,9 @@
 namespace taco {
 namespace {
 
-constexpr int kStageK = 64, kTile = 64, kMaxTokens = 64, kMaxStages = 12, kThreads = 128;
+constexpr int kStageK = 64, kTile = 64, kMaxTokens = 64, kMaxStages = 12, kMaxSplits = 8, kThreads = 128;
 constexpr int kWeightBytes = 2 * kTile * kStageK * 2;   // of a stage: gate, up
-constexpr size_t kSmemBudget = 112 * 1024;              // two CTAs an SM
+constexpr size_t kSmemBudget = 113 * 1024;              // two CTAs an SM
 
 struct ServeArgs {
     void *y;
@@ -37,11 +37,12 @@ struct Barriers {
     uint32_t tmem;
 };
 
-__device__ __forceinline__ float peer_float(uint32_t addr, uint32_t rank)
+// Two floats of shared memory of the cluster's CTA `rank`, at this CTA's address `addr`.
+__device__ __forceinline__ float2 peer_float2(uint32_t addr, uint32_t rank)
 {
-    float v;
-    asm volatile("{\n\t.reg .u32 p;\n\tmapa.shared::cluster.u32 p, %1, %2;\n\tld.shared::cluster.f32 %0, [p];\n\t}"
-                 : "=f"(v)
+    float2 v;
+    asm volatile("{\n\t.reg .u32 p;\n\tmapa.shared::cluster.u32 p, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [p];\n\t}"
+                 : "=f"(v.x), "=f"(v.y)
                  : "r"(addr), "r"(rank)
                  : "memory");
     return v;
@@ -153,25 +154,34 @@ taco_gated_serve_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     // The cluster's CTAs share out the tokens: two columns a thread
     for (int64_t t = static_cast<int64_t>(rank) * 4 + warp; t < a.rows; t += 4ll * a.splits) {
         const int64_t c = n0 + 2 * lane;
-        float z[4] = {};
-        for (int p = 0; p < a.splits; p++)
+        const uint32_t at = base + static_cast<uint32_t>((t * 128 + 2 * lane) * 4);
+        // all CTAs' sums on their way before the first is added
+        float2 gate[kMaxSplits], up[kMaxSplits];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t at = base + static_cast<uint32_t>((t * 128 + (i >> 1) * 64 + 2 * lane + (i & 1)) * 4);
-                z[i] += peer_float(at, a.splits > 1 ? p : rank);
+        for (int p = 0; p < kMaxSplits; p++)
+            if (p < a.splits) {
+                gate[p] = peer_float2(at, p);
+                up[p] = peer_float2(at + 256, p);
+            }
+        float2 g = gate[0], u = up[0];
+#pragma unroll
+        for (int p = 1; p < kMaxSplits; p++)
+            if (p < a.splits) {
+                g = add2(g, gate[p]);
+                u = add2(u, up[p]);
             }
         if (c >= a.inner)
             continue;
         const bool second = c + 1 < a.inner;
         if (a.bias) {
-            z[0] += load_param(a.bias, a.param_dtype, c);
-            z[2] += load_param(a.bias, a.param_dtype, a.inner + c);
+            g.x += load_param(a.bias, a.param_dtype, c);
+            u.x += load_param(a.bias, a.param_dtype, a.inner + c);
             if (second) {
-                z[1] += load_param(a.bias, a.param_dtype, c + 1);
-                z[3] += load_param(a.bias, a.param_dtype, a.inner + c + 1);
+                g.y += load_param(a.bias, a.param_dtype, c + 1);
+                u.y += load_param(a.bias, a.param_dtype, a.inner + c + 1);
             }
         }
-        const float2 y = mul2(activation2<ACT>(make_float2(z[0], z[1])), make_float2(z[2], z[3]));
+        const float2 y = mul2(activation2<ACT>(g), u);
         const uint32_t w = a.f16 ? float2_to_f16x2(y.x, y.y) : float2_to_bf16x2(y.x, y.y);
         uint16_t *to = static_cast<uint16_t *>(a.y) + t * a.inner + c;
         if (a.inner % 2 == 0) {
@@ -211,9 +221,8 @@ cudaError_t launch_gated_serve(const GatedArgs &a, const void *x, const void *w,
                    0, static_cast<int>((a.hidden + kStageK - 1) / kStageK), 1};
     const int stage_bytes = kWeightBytes + args.tokens * kStageK * 2;
     const int64_t tiles = (a.inner + kTile - 1) / kTile;
-    while (args.splits < 8 && tiles * args.splits * 2 <= 2 * sms && args.stages_total >= args.splits * 4)
-        args.splits *= 2;
-    args.stages = std::max(2, std::min({kMaxStages, static_cast<int>((kSmemBudget - 2048) / stage_bytes),
+    args.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, 2 * sms / tiles, args.stages_total / 4})));
+    args.stages = std::max(2, std::min({kMaxStages, static_cast<int>((kSmemBudget - 1280) / stage_bytes),
                                         (args.stages_total + args.splits - 1) / args.splits}));
     const CUtensorMapDataType type = args.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     alignas(64) CUtensorMap map_w, map_x;

@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
 #pragma unroll
     for (int j = 0; j < NV; j++)
         col[j] = (v0 + 32 * j) * 8 - shift;
-    const int64_t first = blockIdx.x + static_cast<int64_t>(gridDim.x) * group, step = static_cast<int64_t>(gridDim.x) * groups;
+    const int64_t first = ODD ? blockIdx.x + static_cast<int64_t>(gridDim.x) * group : static_cast<int64_t>(blockIdx.x) * groups + group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     if (warp == 0 && lane < 2 && !ODD && first + lane * step < a.rows) {
         // the group's first rows on their way to L2 while the kernel before still runs
         const int64_t at = (first + lane * step) * C;
