@@ -263,6 +263,8 @@ def gated_linear_backward(dy: torch.Tensor, packed: torch.Tensor, weight: Option
         y = torch.empty_like(dy) if recompute else None
         dbias = torch.empty(2 * inner, dtype=bias_dtype, device=dy.device) if bias_dtype is not None else None
         nbytes = _workspace_bytes("taco_gated_linear_backward_workspace", rows, inner, hidden)
+        if bias_dtype is None:   # without the bias gradient's part
+            nbytes -= _workspace_bytes("taco_gated_linear_backward_workspace", rows, inner, 0)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
         rc = lib.taco_gated_linear_backward(
             _pack_gated_backward(dy.data_ptr(), ppacked, pw, dz.data_ptr(), _address(dx), _address(y), _address(dbias),

@@ -21,6 +21,8 @@ struct DeviceState {
     int ctas_per_sm = 0;        // last occupancy query (set-up check only)
     std::once_flag train_once;  // set-up of the training operators' kernels
     cudaError_t train_error = cudaSuccess;
+    std::once_flag rms_once, gated_once;
+    cudaError_t rms_error = cudaSuccess, gated_error = cudaSuccess;
 };
 
 // Set-up of the current device, once per device and process.

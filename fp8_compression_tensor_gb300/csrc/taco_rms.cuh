@@ -21,14 +21,18 @@ namespace {
 // The first of the row's columns in the group's vector v, and whether the vector reaches outside the row.
 __device__ __forceinline__ bool at_edge(int c, int C) { return c < 0 || c + 8 > C; }
 
-// Zeros for what lies outside the row.
-__device__ __forceinline__ void mask_edge(F8 &f, int c, int C)
+// Zeros for what lies outside the row in `tensors` pieces of a vector whose first column is c, `pitch` bytes apart and
+// each in units of 16 bytes `unit` apart (shared memory, this thread's own copies).
+template <typename T>
+__device__ __forceinline__ void clear_edge(uint8_t *piece, int tensors, int pitch, int unit, int c, int C)
 {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        f.v[i].x = c + 2 * i >= 0 && c + 2 * i < C ? f.v[i].x : 0.f;
-        f.v[i].y = c + 2 * i + 1 >= 0 && c + 2 * i + 1 < C ? f.v[i].y : 0.f;
-    }
+    constexpr int kPerUnit = 16 / sizeof(T);
+#pragma unroll 1
+    for (int t = 0; t < tensors; t++, piece += pitch)
+#pragma unroll 1
+        for (int i = 0; i < 8; i++)
+            if (c + i < 0 || c + i >= C)
+                reinterpret_cast<T *>(piece + i / kPerUnit * unit)[i % kPerUnit] = from_float<T>(0.f);
 }
 
 // Stores column c on of the row at `row`, element by element inside the row.

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kRmsThreads, 1) taco_rms_kernel(RmsArgs a, int
     const int C = static_cast<int>(a.hidden), unit = blockDim.x * 16, vectors = row_vectors(C);
     const int shift = ODD ? static_cast<int>(blockIdx.x * a.hidden & 7) : 0;
     float *sparam = reinterpret_cast<float *>(dynamic);
-    const uint8_t *ring = dynamic + (STAGED ? 32 * vectors : 0) + threadIdx.x * 16;
+    uint8_t *ring = dynamic + (STAGED ? 32 * vectors : 0) + threadIdx.x * 16;
     const uint32_t ring_at = smem_addr(ring);
     const int row_units = (a.residual ? 2 : 1) * NV * kUnits;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
@@ -167,6 +167,10 @@ __global__ void __launch_bounds__(kRmsThreads, 1) taco_rms_kernel(RmsArgs a, int
 #pragma unroll
     for (int j = 0; j < NV; j++)
         col[j] = (v0 + 32 * j) * 8 - shift;
+    bool edges = false;   // whether one of this thread's vectors reaches outside the row
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+        edges = edges || (ODD && col[j] < C && at_edge(col[j], C));
     const int64_t first = ODD ? blockIdx.x + static_cast<int64_t>(gridDim.x) * group : static_cast<int64_t>(blockIdx.x) * groups + group;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     if (warp == 0 && lane < 2 && !ODD && first + lane * step < a.rows) {
@@ -179,6 +183,8 @@ __global__ void __launch_bounds__(kRmsThreads, 1) taco_rms_kernel(RmsArgs a, int
     const int64_t end = a.rows * a.hidden * static_cast<int>(sizeof(T));   // of the tensors, in bytes
     auto copy_row = [&](int64_t row, int stage) {
         if (row < a.rows) {
+            // the tensors' last vector may end behind them
+            const bool whole = !ODD || (row * C - shift + 8 * vectors) * static_cast<int>(sizeof(T)) <= end;
             uint32_t to = ring_at + static_cast<uint32_t>(stage * row_units * unit);
             auto piece = [&](const T *src) {
 #pragma unroll
@@ -187,12 +193,11 @@ __global__ void __launch_bounds__(kRmsThreads, 1) taco_rms_kernel(RmsArgs a, int
                     for (int k = 0; k < kUnits; k++, to += unit)
                         if (FULL || col[j] < C) {
                             const T *from = src + row * C + col[j] + 8 / kUnits * k;
-                            if (ODD) {
-                                // the tensor's last vector may end behind it
+                            if (!ODD || whole) {
+                                copy16<T>(to, from);
+                            } else {
                                 const int64_t left = end - (row * C + col[j]) * static_cast<int>(sizeof(T)) - 16 * k;
                                 copy16_upto<T>(to, left > 0 ? from : src, left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0);
-                            } else {
-                                copy16<T>(to, from);
                             }
                         }
             };
@@ -220,8 +225,14 @@ __global__ void __launch_bounds__(kRmsThreads, 1) taco_rms_kernel(RmsArgs a, int
         copy_row(row + (stages - 1) * step, fill);
         fill = fill + 1 == stages ? 0 : fill + 1;
         copies_landed(stages - 1);
-        const uint8_t *mine = ring + static_cast<size_t>(stage) * row_units * unit;
+        uint8_t *mine = ring + static_cast<size_t>(stage) * row_units * unit;
         stage = stage + 1 == stages ? 0 : stage + 1;
+        if (ODD && edges) {
+#pragma unroll
+            for (int j = 0; j < NV; j++)
+                if (col[j] < C && at_edge(col[j], C))
+                    clear_edge<T>(mine + j * kUnits * unit, res ? 2 : 1, NV * kUnits * unit, unit, col[j], C);
+        }
         F8 h[NV];
         float2 squares = both(0.f);
 #pragma unroll
@@ -243,8 +254,6 @@ __global__ void __launch_bounds__(kRmsThreads, 1) taco_rms_kernel(RmsArgs a, int
                     store_vector<T, ODD>(static_cast<T *>(a.summed) + row * C, h[j], col[j], C);
                     h[j] = unpack(pack<T>(h[j]));
                 }
-                if (ODD && at_edge(col[j], C))
-                    mask_edge(h[j], col[j], C);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
                     squares = fma2(h[j].v[i], h[j].v[i], squares);
@@ -305,7 +314,7 @@ constexpr int kRmsVectors = kRmsThreads * 4;
 template <typename T>
 bool rms_registers(const RmsArgs &a, int sms, cudaStream_t stream, cudaError_t *result)
 {
-    if (row_vectors(a.hidden) > kRmsVectors)
+    if (a.hidden > 8 * kRmsVectors || row_vectors(a.hidden) > kRmsVectors)
         return false;
     RmsArgs args = a;
     const int vectors = row_vectors(a.hidden), nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;

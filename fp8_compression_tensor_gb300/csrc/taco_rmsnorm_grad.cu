@@ -188,6 +188,10 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
 #pragma unroll
     for (int j = 0; j < NV; j++)
         col[j] = (v0 + 32 * j) * 8 - shift;
+    bool edges = false;   // whether one of this thread's vectors reaches outside the row
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+        edges = edges || (ODD && col[j] < C && at_edge(col[j], C));
     const int64_t first = ODD ? blockIdx.x + static_cast<int64_t>(gridDim.x) * group : static_cast<int64_t>(blockIdx.x) * groups + group;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     if (warp == 0 && lane < 2 && !ODD && first + lane * step < a.rows) {
@@ -203,6 +207,8 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
     const int64_t end = a.rows * a.hidden * static_cast<int>(sizeof(T));   // of the tensors, in bytes
     auto copy_row = [&](int64_t row, int stage) {
         if (row < a.rows) {
+            // the tensors' last vector may end behind them
+            const bool whole = !ODD || (row * C - shift + 8 * vectors) * static_cast<int>(sizeof(T)) <= end;
             uint32_t to = ring_at + static_cast<uint32_t>(stage * stage_bytes) + threadIdx.x * 16u;
             auto piece = [&](const void *tensor) {
                 const T *src = static_cast<const T *>(tensor);
@@ -212,12 +218,11 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
                     for (int k = 0; k < kUnits; k++, to += unit)
                         if (FULL || col[j] < C) {
                             const T *from = src + row * C + col[j] + 8 / kUnits * k;
-                            if (ODD) {
-                                // the tensor's last vector may end behind it
+                            if (!ODD || whole) {
+                                copy16<T>(to, from);
+                            } else {
                                 const int64_t left = end - (row * C + col[j]) * static_cast<int>(sizeof(T)) - 16 * k;
                                 copy16_upto<T>(to, left > 0 ? from : src, left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0);
-                            } else {
-                                copy16<T>(to, from);
                             }
                         }
             };
@@ -261,21 +266,24 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
             copy_row(row + (stages - 1) * step, fill);
             copies_landed(stages - 1);
         }
-        const uint8_t *mine = ring + static_cast<size_t>(stage) * stage_bytes + threadIdx.x * 16;
+        uint8_t *mine = ring + static_cast<size_t>(stage) * stage_bytes + threadIdx.x * 16;
         const uint8_t *rec = ring + static_cast<size_t>(stage) * stage_bytes + row_units * unit + group * record_room +
                              (RECORDS ? row * pitch & 15 : 0);
         stage = stage + 1 == stages ? 0 : stage + 1;
         const float rstd = next_rstd;
         fetch(row + step);
+        if (ODD && edges) {
+#pragma unroll
+            for (int j = 0; j < NV; j++)
+                if (col[j] < C && at_edge(col[j], C))
+                    clear_edge<T>(mine + j * kUnits * unit, 2, NV * kUnits * unit, unit, col[j], C);
+        }
         auto vector = [&](int tensor, int j) {
             Raw8<T> v;
 #pragma unroll
             for (int k = 0; k < kUnits; k++)
                 v.v[k] = *reinterpret_cast<const uint4 *>(mine + ((tensor * NV + j) * kUnits + k) * unit);
-            F8 f = unpack(v);
-            if (ODD && at_edge(col[j], C))
-                mask_edge(f, col[j], C);
-            return f;
+            return unpack(v);
         };
         // xhat = q f: codes and their block's scale, or x and rstd
         float factor[NV];
@@ -401,7 +409,7 @@ bool rms_grad_shared(RmsGradArgs *a, int sms, cudaStream_t stream, cudaError_t *
 {
     const int64_t C = a->hidden;
     const bool records = !a->x, odd = C % 8 != 0;
-    if (row_vectors(C) > kRmsGradThreads * 4)
+    if (C > 32 * kRmsGradThreads || row_vectors(C) > 4 * kRmsGradThreads)
         return false;
     const int vectors = row_vectors(C), nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;
     int warps = (vectors + 32 * nv - 1) / (32 * nv);

@@ -77,15 +77,33 @@ taco_status_t training_device(DeviceState **out)
             e = init_norm();
         if (e == cudaSuccess)
             e = init_norm_grad();
-        if (e == cudaSuccess)
-            e = init_rms();
-        if (e == cudaSuccess)
-            e = init_rms_grad();
-        if (e == cudaSuccess)
-            e = init_gated();
         dev->train_error = e;
     });
     return dev->train_error == cudaSuccess ? TACO_OK : cuda_fail(dev->train_error);
+}
+
+// The same for the RMS norm and for the gated layer, whose kernels a program without them does not load.
+taco_status_t rms_device(DeviceState **out)
+{
+    const taco_status_t st = device_state(out);
+    if (st != TACO_OK)
+        return st;
+    DeviceState *dev = *out;
+    std::call_once(dev->rms_once, [dev] {
+        const cudaError_t e = init_rms();
+        dev->rms_error = e == cudaSuccess ? init_rms_grad() : e;
+    });
+    return dev->rms_error == cudaSuccess ? TACO_OK : cuda_fail(dev->rms_error);
+}
+
+taco_status_t gated_device(DeviceState **out)
+{
+    const taco_status_t st = device_state(out);
+    if (st != TACO_OK)
+        return st;
+    DeviceState *dev = *out;
+    std::call_once(dev->gated_once, [dev] { dev->gated_error = init_gated(); });
+    return dev->gated_error == cudaSuccess ? TACO_OK : cuda_fail(dev->gated_error);
 }
 
 // The gated layer's sizes: elements of [rows, inner], [rows, hidden] and [2 inner, hidden] in range.
@@ -371,7 +389,7 @@ taco_status_t taco_rmsnorm(const taco_rmsnorm_args_t *a, taco_stream_t stream)
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = training_device(&dev)) != TACO_OK)
+    if ((st = rms_device(&dev)) != TACO_OK)
         return st;
     const RmsArgs k{a->x,    a->residual, a->weight, a->y,  a->summed,      a->rstd,  static_cast<uint8_t *>(a->packed),
                     static_cast<uint8_t *>(a->packed_y), a->rows, a->hidden, a->eps, a->param_dtype, a->block, a->code};
@@ -420,7 +438,7 @@ taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t *a, taco_
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = training_device(&dev)) != TACO_OK)
+    if ((st = rms_device(&dev)) != TACO_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     float *ws = a->dweight ? static_cast<float *>(a->workspace) : nullptr;
@@ -470,7 +488,7 @@ taco_status_t taco_gated_linear(const taco_gated_linear_args_t *a, taco_stream_t
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = training_device(&dev)) != TACO_OK)
+    if ((st = gated_device(&dev)) != TACO_OK)
         return st;
     const GatedArgs k{a->x, a->weight, a->bias, a->y, static_cast<uint8_t *>(a->packed), a->workspace, a->rows, a->inner,
                       a->hidden, a->dtype, a->param_dtype, a->activation, a->block, a->code};
@@ -524,7 +542,7 @@ taco_status_t taco_gated_linear_backward(const taco_gated_linear_backward_args_t
     if ((st = check_spans(spans)) != TACO_OK)
         return st;
     DeviceState *dev = nullptr;
-    if ((st = training_device(&dev)) != TACO_OK)
+    if ((st = gated_device(&dev)) != TACO_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     float *parts = sums > 0 ? reinterpret_cast<float *>(static_cast<uint8_t *>(a->workspace) + product) : nullptr;

@@ -381,7 +381,9 @@ TACO_API taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t 
  *   y = act(z_gate) z_up,  and the records of z, [rows, 2 inner] (inner % block == 0
  * then, blocks 32, 64 and 128).  The activation: silu(g) = g / (1 + exp(-g)),
  * or GELU in either form.  bf16 and f16; x and W have one type.
- * hidden >= 1.  rows == 0 or inner == 0 launches nothing.
+ * 1 <= hidden < 2^31 - 256, rows < 2^31 - 256, inner < 2^30 - 256
+ * (TACO_ERR_BAD_SHAPE).  rows == 0 or inner == 0 launches nothing.  Rows of x and W
+ * whose hidden is no multiple of 8 are first copied to the workspace.
  */
 typedef enum taco_activation {
     TACO_ACTIVATION_SILU = 0,
@@ -412,7 +414,7 @@ TACO_API taco_status_t taco_gated_linear(const taco_gated_linear_args_t *args, t
  *   dbias = sum over rows of dz (before rounding), and y again.
  * dx is the product of dz as it is written (rounded to dtype).  The weight's
  * gradient dz^T X is taco_weight_grad's (`out` = 2 inner).  inner >= 1, and
- * hidden >= 1 where dx is wanted.
+ * hidden >= 1 where dx is wanted; the ranges are those above.
  */
 typedef struct taco_gated_linear_backward_args {
     const void *dy;             /* in:  [rows, inner] */
@@ -430,7 +432,8 @@ typedef struct taco_gated_linear_backward_args {
     int block, code;
 } taco_gated_linear_backward_args_t;
 
-/* Bytes for a call that wants dbias and, with hidden > 0, dx; -1: bad shape. */
+/* Bytes for a call that wants dbias and, with hidden > 0, dx; -1: bad shape.  A call without dbias needs as many fewer as
+ * the answer for hidden = 0. */
 TACO_API int64_t taco_gated_linear_backward_workspace(int64_t rows, int64_t inner, int64_t hidden);
 TACO_API taco_status_t taco_gated_linear_backward(const taco_gated_linear_backward_args_t *args, taco_stream_t stream);
 
