@@ -15,9 +15,13 @@
 // even CTA's barrier.  Two accumulators of 256 tensor-memory columns take turns, so
 // the epilogue of a tile runs beside the next one's products.
 //
-// Roles (384 threads): warp 0 loads, warp 1 of the even CTA issues the products,
-// warp 2 owns tensor memory, warps 4-11 are the epilogue: warp w reads lanes 32 (w
-// % 4) .., a row a thread.
+// Roles (512 threads): warp 0 loads, warp 1 of the even CTA issues the products,
+// warp 2 owns tensor memory, warps 4-15 are the epilogue: warp w reads lanes 32 (w
+// % 4) .., a row a thread.  Without records the first eight of them take 64 columns
+// of y (128 of dx) each; with records the first four take y, the others the gate's
+// and the up projection's records: 333 x 1000 x 2048 f16 with biases takes 12.9 us
+// and 8192 x 1024 x 4096 with biases 97, with eight warps that do both in turn 13.9
+// and 116.
 #include <algorithm>
 #include <climits>
 
@@ -33,9 +37,12 @@ constexpr int kStageK = 64;                   // of the sum per pipeline stage
 constexpr int kStages = 5;
 constexpr int kOperandBytes = 128 * kStageK * 2, kStageBytes = 2 * kOperandBytes;   // of one CTA
 constexpr int kHalfBytes = 64 * kStageK * 2;                                        // 64 columns of an N-major B
-constexpr int kWarpBytes = 8192;              // an epilogue warp's buffer for what it writes
-constexpr int kThreads = 384;
+// An epilogue warp's buffer for what it writes, and behind it the bias of its columns.
+constexpr int kWarpBytes = 8192, kBiasAt = 6144;                                    // one of eight, without records
+constexpr int kOutBytes = 4096 + 1024, kRecordBytes = 5120, kRecordWarpBytes = kRecordBytes + 512;   // four and eight, with records
+constexpr int kThreads = 512;
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + 8 * kWarpBytes;
+static_assert(4 * kOutBytes + 8 * kRecordWarpBytes <= 8 * kWarpBytes, "buffers");
 constexpr int kInputGrad = -1;                // in the place of an activation: dx = dz W
 
 struct Barriers {
@@ -142,26 +149,23 @@ __device__ __forceinline__ void write_staged(uint32_t buffer, const void *map, c
     __syncwarp();
 }
 
-// The bias of a tile's 128 gate and 128 up columns from c on, as binary32 in the
-// warp's buffer behind what it writes (zeros outside).  It is fetched ahead of the
+// The bias of a tile's 128 columns from c on, of projection k (0 gate, 1 up), as
+// binary32 at `to` in shared memory (zeros outside).  It is fetched ahead of the
 // accumulator's wait: loaded a column a lane where it is added, 333 x 1000 x 2048 with
 // records took 17 us.
-constexpr int kBiasAt = 6144;
-
-__device__ __forceinline__ void stage_bias(uint32_t buffer, const TileArgs &a, int64_t c)
+__device__ __forceinline__ void stage_bias(uint32_t to, const TileArgs &a, int k, int64_t c)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int64_t col = c + 32 * (i & 3) + lane;
-        const float v = col < a.width ? load_param(a.bias, a.param_dtype, (i >> 2) * a.width + col) : 0.f;
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(buffer + kBiasAt + (32 * i + lane) * 4), "f"(v) : "memory");
+    for (int i = 0; i < 4; i++) {
+        const int64_t col = c + 32 * i + lane;
+        const float v = col < a.width ? load_param(a.bias, a.param_dtype, k * a.width + col) : 0.f;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + (32 * i + lane) * 4), "f"(v) : "memory");
     }
-    __syncwarp();
 }
 
-// 32 accumulators, as loaded, of this thread's row, and the bias of column `at` of the tile's 256 on.
-__device__ __forceinline__ void to_z(uint32_t (&r)[32], const TileArgs &a, uint32_t buffer, int at, float (&z)[32])
+// 32 accumulators of this thread's row, as loaded, and their columns' staged bias.
+__device__ __forceinline__ void to_z(uint32_t (&r)[32], const TileArgs &a, uint32_t bias, float (&z)[32])
 {
     tmem_regs_ready(r);
 #pragma unroll
@@ -170,7 +174,7 @@ __device__ __forceinline__ void to_z(uint32_t (&r)[32], const TileArgs &a, uint3
     if (a.bias) {
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-            const float4 v = lds_float4(buffer + kBiasAt + (at + i) * 4);
+            const float4 v = lds_float4(bias + i * 4);
             z[i] += v.x;
             z[i + 1] += v.y;
             z[i + 2] += v.z;
@@ -179,12 +183,12 @@ __device__ __forceinline__ void to_z(uint32_t (&r)[32], const TileArgs &a, uint3
     }
 }
 
-__device__ __forceinline__ void load_z(uint32_t acc, const TileArgs &a, uint32_t buffer, int at, float (&z)[32])
+__device__ __forceinline__ void load_z(uint32_t from, const TileArgs &a, uint32_t bias, float (&z)[32])
 {
     uint32_t r[32];
-    tmem_ld32(acc + at, r);
+    tmem_ld32(from, r);
     tmem_ld_wait();
-    to_z(r, a, buffer, at, z);
+    to_z(r, a, bias, z);
 }
 
 template <int CODE>
@@ -200,14 +204,20 @@ __device__ __forceinline__ void encode_row32(const float (&z)[32], float inv, ui
 }
 
 // Records of 128 columns of one projection (k: 0 gate, 1 up) from column c on, 32
-// rows from `row` on.  A block's accumulators are read twice, for its maximum and
-// for its codes.  The rows' record bytes go through the buffer, an odd number of
-// eight bytes apart, and out in row order.
-__device__ __forceinline__ void write_tile_records(uint32_t acc, uint32_t buffer, const TileArgs &a, int k, int64_t row, int64_t c)
+// rows from `row` on; `acc` the first column's accumulators, `bias` its staged bias.
+// A block's accumulators are read twice, for its maximum and for its codes.  The
+// rows' record bytes go through the buffer (at an odd number of eight bytes apart,
+// which the banks like, but for blocks of 32, which fill it) and out in row order.
+// The tensor core takes nearly all of shared memory's bandwidth, so what goes
+// through the buffers is what an epilogue costs: of 8192 x 1024 x 4096 y takes 4 us
+// and the records 14, of 70 without either.  16 bytes a lane on the way out took as
+// long.
+__device__ __forceinline__ void write_tile_records(uint32_t acc, uint32_t bias, uint32_t buffer, const TileArgs &a, int k, int64_t row,
+                                                   int64_t c)
 {
     const int lane = threadIdx.x & 31, shift = 31 - __clz(a.block), block = a.block;
     const int cols = static_cast<int>(a.width - c < 128 ? a.width - c : 128);
-    const uint32_t pitch = (16 + (128 >> shift) | 1) * 8;
+    const uint32_t pitch = block == 32 ? 160 : (16 + (128 >> shift) | 1) * 8;
     uint32_t to = buffer + lane * pitch;
 #pragma unroll 1
     for (int b = 0; b < cols; b += block) {
@@ -215,7 +225,7 @@ __device__ __forceinline__ void write_tile_records(uint32_t acc, uint32_t buffer
         float z[32], inv;
 #pragma unroll 1
         for (int j = b; j < b + block; j += 32) {
-            load_z(acc, a, buffer, k * 128 + j, z);
+            load_z(acc + j, a, bias + j * 4, z);
 #pragma unroll
             for (int i = 0; i < 32; i++)
                 top = max(top, abs_bits(z[i]));
@@ -224,7 +234,7 @@ __device__ __forceinline__ void write_tile_records(uint32_t acc, uint32_t buffer
 #pragma unroll 1
         for (int j = b; j < b + block; j += 32, to += 32) {
             if (block > 32)
-                load_z(acc, a, buffer, k * 128 + j, z);
+                load_z(acc + j, a, bias + j * 4, z);
             if (a.code == 0)
                 encode_row32<0>(z, inv, to);
             else if (a.code == 1)
@@ -274,7 +284,7 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(bar(bars.acc_full[b]), 1);
-            mbar_init(bar(bars.acc_empty[b]), 16);   // eight epilogue warps of each CTA
+            mbar_init(bar(bars.acc_empty[b]), a.packed ? 24 : 16);   // the epilogue warps of both CTAs
         }
         mbar_init(bar(bars.drained), 1);
         fence_mbar_init();
@@ -371,32 +381,41 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             own_commit(bar(bars.drained));
             mbar_wait_bounded_thread(bar(bars.drained), 0, fault, kFaultGated);
         }
-    } else if (warp >= 4) {
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t empty0 = in_even_cta(bar(bars.acc_empty[0]));
-        const uint32_t buffer = base + kStages * kStageBytes + (warp - 4) * kWarpBytes;
+    } else if (warp >= 4 && (warp < 12 || a.packed)) {
+        const int quarter = warp & 3, team = (warp - 4) >> 2;
+        const bool records = ACT != kInputGrad && a.packed;
+        const bool out = !records || team == 0;                   // writes y or dx, not records
+        const uint32_t empty0 = in_even_cta(bar(bars.acc_empty[0])), buffers = base + kStages * kStageBytes;
+        const uint32_t buffer = !records ? buffers + (warp - 4) * kWarpBytes
+                                : out    ? buffers + quarter * kOutBytes
+                                         : buffers + 4 * kOutBytes + (warp - 8) * kRecordWarpBytes;
+        const uint32_t bias = buffer + (!records ? kBiasAt : out ? 4096 : kRecordBytes);
         uint32_t turn = 0;
         for (int64_t u = first_unit; u < plan.units; u += step_units, turn++) {
             int m, n, first, count;
             int64_t part;
             plan.at(u, m, n, part, first, count);
             const uint32_t b = turn & 1u;
-            if (ACT != kInputGrad && a.bias)
-                stage_bias(buffer, a, static_cast<int64_t>(n) * 128);
+            if (ACT != kInputGrad && a.bias) {
+                stage_bias(bias, a, out ? 0 : team - 1, static_cast<int64_t>(n) * 128);
+                if (out)
+                    stage_bias(bias + 512, a, 1, static_cast<int64_t>(n) * 128);
+                __syncwarp();
+            }
             if (!mbar_wait_bounded(bar(bars.acc_full[b]), (turn >> 1) & 1u, fault, kFaultGated))
                 break;
             tc_fence_after_sync();
             const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + b * 256;
             const int row0 = static_cast<int>(rank) * 128 + quarter * 32;
             const int64_t row = static_cast<int64_t>(m) * kTileM + row0;
-            bulk_wait_read<0>();   // (the lane that stored) the buffer's last tile is on its way
-            __syncwarp();
             if (ACT == kInputGrad && part >= 0) {
                 // 32 columns at a time, turned so that eight lanes write 128 consecutive bytes
-                float *to = a.parts + (part * kTileM + row0) * 256 + half * 128;
+                float *to = a.parts + (part * kTileM + row0) * 256 + team * 128;
+                bulk_wait_read<0>();   // (the lane that stored) the buffer's last tile is on its way
+                __syncwarp();
                 for (int c = 0; c < 4; c++) {
                     float z[32];
-                    load_z(acc, a, buffer, half * 128 + c * 32, z);
+                    load_z(acc + team * 128 + c * 32, a, 0, z);
 #pragma unroll
                     for (int i = 0; i < 8; i++)
                         sts128(buffer + lane * 128 + ((i ^ (lane & 7)) << 4),
@@ -412,41 +431,45 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     __syncwarp();
                 }
             } else if (ACT == kInputGrad) {
+                bulk_wait_read<0>();
+                __syncwarp();
                 for (int c = 0; c < 2; c++) {
                     const uint32_t place = buffer + c * 4096;
                     for (int j = 0; j < 2; j++) {
                         float z[32];
-                        load_z(acc, a, buffer, half * 128 + c * 64 + j * 32, z);
+                        load_z(acc + team * 128 + c * 64 + j * 32, a, 0, z);
                         stage_row32(place, lane, j, z, a.f16);
                     }
-                    write_staged(place, &map_out, a, row, static_cast<int64_t>(n) * 256 + half * 128 + c * 64);
+                    write_staged(place, &map_out, a, row, static_cast<int64_t>(n) * 256 + team * 128 + c * 64);
                 }
-            } else {
+            } else if (out) {
                 const int64_t c0 = static_cast<int64_t>(n) * 128;
+                const int begin = records ? 0 : team * 64, end = records ? 128 : begin + 64;
 #pragma unroll 1
-                for (int j = 0; j < 2; j++) {
-                    const int c = half * 64 + j * 32;
+                for (int c = begin; c < end; c += 32) {
+                    if (c % 64 == 0) {
+                        bulk_wait_read<0>();   // (the lane that stored) what the buffer held last is on its way
+                        __syncwarp();
+                    }
                     uint32_t rg[32], ru[32];
                     tmem_ld32(acc + c, rg);
                     tmem_ld32(acc + 128 + c, ru);
                     tmem_ld_wait();
                     float g[32], v[32];
-                    to_z(rg, a, buffer, c, g);
-                    to_z(ru, a, buffer, 128 + c, v);
+                    to_z(rg, a, bias + c * 4, g);
+                    to_z(ru, a, bias + 512 + c * 4, v);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         const float2 y = mul2(activation2<ACT == kInputGrad ? 0 : ACT>(make_float2(g[i], g[i + 1])), make_float2(v[i], v[i + 1]));
                         v[i] = y.x;
                         v[i + 1] = y.y;
                     }
-                    stage_row32(buffer, lane, j, v, a.f16);
+                    stage_row32(buffer, lane, c >> 5 & 1, v, a.f16);
+                    if (c % 64)
+                        write_staged(buffer, &map_out, a, row, c0 + c - 32);
                 }
-                write_staged(buffer, &map_out, a, row, c0 + half * 64);
-                if (a.packed) {
-                    bulk_wait_read<0>();
-                    __syncwarp();
-                    write_tile_records(acc, buffer, a, half, row, c0);
-                }
+            } else {
+                write_tile_records(acc + (team - 1) * 128, bias, buffer, a, team - 1, row, static_cast<int64_t>(n) * 128);
             }
             tc_fence_before_sync();
             __syncwarp();
