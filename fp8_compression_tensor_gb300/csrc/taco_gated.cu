@@ -578,7 +578,7 @@ cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStrea
         x = ws;
         w = ws + 2 * a.rows * pitch;
     }
-    if (e == cudaSuccess && !a.packed && gated_serves(a.rows))
+    if (e == cudaSuccess && !a.packed && gated_serves(a.rows, a.inner))
         return launch_gated_serve(a, x, w, pitch, fault, sms, stream);
     const CUtensorMapDataType type = a.dtype == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     alignas(64) CUtensorMap map_x, map_w, map_y = {};

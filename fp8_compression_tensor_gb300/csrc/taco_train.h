@@ -155,7 +155,7 @@ bool gated_in_range(int64_t rows, int64_t inner, int64_t hidden);
 cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
 // The layer of few rows; x and w with rows `pitch` elements apart.
 cudaError_t init_gated_serve();
-bool gated_serves(int64_t rows);
+bool gated_serves(int64_t rows, int64_t inner);
 cudaError_t launch_gated_serve(const GatedArgs &a, const void *x, const void *w, int64_t pitch, uint32_t *fault, int sms, cudaStream_t stream);
 cudaError_t launch_gated_input_grad(const GatedInputGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
 

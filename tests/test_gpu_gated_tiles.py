@@ -42,3 +42,16 @@ def test_long_sums(taco):  # noqa: F811
     y, off_y = gr.gated(z, off, "silu")
     ref.within(taco.gated_linear(x.cuda(), w.cuda()).y, y, off_y, what="few rows")
     ref.within(taco.gated_linear(x.cuda(), w.cuda(), checkpoint=True).y, y, off_y, what="pairs")
+
+
+@pytest.mark.parametrize("rows", (65, 112, 128))
+@pytest.mark.parametrize("inner", (12288, 12296, 12417))
+def test_few_rows_at_the_last_width(taco, rows, inner):  # noqa: F811
+    """Both sides of the width up to which 65 to 128 rows go to the few-row kernel."""
+    check_forward(taco, rows, 72, inner, BF16, "silu", F32)
+
+
+def test_few_rows_in_clusters(taco):  # noqa: F811
+    """Every number of CTAs a cluster: 1 to 8 along K."""
+    for inner in (30 * 64, 38 * 64, 45 * 64, 54 * 64, 68 * 64, 90 * 64, 136 * 64, 137 * 64, 280 * 64):
+        check_forward(taco, 5, 2072, inner, F16, "gelu")
