@@ -160,10 +160,13 @@ __global__ void __launch_bounds__(128) taco_rms_grad_wide_columns_kernel(RmsGrad
 // the one of the row sum of the row before, ahead of which each thread waits for
 // its part of the next row.  A row's place is filled again behind the barrier of
 // the row after it, when every thread has left it.
+// DIRECT: dsummed does not come to shared memory, where the rows would no longer
+// fit, but to L2 a row ahead and is loaded where it is added.  8192 x 11648 bf16 from
+// records with dsummed takes 188 us so, and 309 with rows read twice.
 // CODE: code format of the records, or -1 to read x.  ODD and FULL as forward.
 constexpr int kRmsGradThreads = 512;
 
-template <typename T, int NV, int CODE, bool ODD, bool FULL>
+template <typename T, int NV, int CODE, bool ODD, bool FULL, bool DIRECT>
 __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGradArgs a, int warps, int groups, int stages)
 {
     extern __shared__ __align__(16) uint8_t dynamic[];   // weight, then the copies; then the groups' column sums
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
     const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
     const int C = static_cast<int>(a.hidden), unit = blockDim.x * 16, vectors = row_vectors(C);
     const int shift = ODD ? static_cast<int>(blockIdx.x * a.hidden & 7) : 0;
-    const int row_units = (1 + !RECORDS + (a.dsummed != nullptr)) * NV * kUnits;
+    const int row_units = (1 + !RECORDS + (!DIRECT && a.dsummed)) * NV * kUnits;
     const int block_log = RECORDS ? 31 - __clz(a.block) : 0;
     const int64_t pitch = RECORDS ? static_cast<int64_t>(C >> block_log) * (a.block + 8) : 0;
     const int record_room = RECORDS ? static_cast<int>(pitch + 8 + 15) / 16 * 16 : 0;     // of one group's row
@@ -229,8 +232,10 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
             piece(a.dy);
             if (!RECORDS)
                 piece(a.x);
-            if (a.dsummed)
+            if (!DIRECT && a.dsummed)
                 piece(a.dsummed);
+            if (DIRECT && warp == 0 && lane == 0)
+                bulk_prefetch_l2(static_cast<const T *>(a.dsummed) + row * C, C * static_cast<int>(sizeof(T)));
             if (RECORDS) {
                 const int64_t at = row * pitch & ~int64_t{15}, left = a.rows * pitch - at;
                 const int bytes = static_cast<int>((row + 1) * pitch - at);
@@ -329,8 +334,8 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
                     dw[j].v[i] = fma2(mul2(g.v[i], both(factor[j])), q.v[i], dw[j].v[i]);
                     w.v[i] = mul2(fma2(q.v[i], both(-c * factor[j]), mul2(w.v[i], g.v[i])), both(rstd));
                 }
-                if (a.dsummed) {
-                    const F8 d = vector(RECORDS ? 1 : 2, j);
+                if (DIRECT || a.dsummed) {
+                    const F8 d = DIRECT ? unpack(load_raw8(static_cast<const T *>(a.dsummed) + row * C + col[j])) : vector(RECORDS ? 1 : 2, j);
 #pragma unroll
                     for (int i = 0; i < 4; i++)
                         w.v[i] = add2(w.v[i], d.v[i]);
@@ -384,10 +389,19 @@ __global__ void __launch_bounds__(kRmsGradThreads, 1) taco_rms_grad_kernel(RmsGr
 template <typename T, int CODE>
 const void *rms_grad_kernel(int nv, bool full)
 {
-    return nv == 1   ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 1, CODE, false, false>)
-           : nv == 2 ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 2, CODE, false, false>)
-           : full    ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, CODE, false, true>)
-                     : reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, CODE, false, false>);
+    return nv == 1   ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 1, CODE, false, false, false>)
+           : nv == 2 ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 2, CODE, false, false, false>)
+           : full    ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, CODE, false, true, false>)
+                     : reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, CODE, false, false, false>);
+}
+
+// From records with dsummed loaded where it is added (wide rows: four vectors a lane).
+template <typename T>
+const void *rms_grad_direct_kernel(int code)
+{
+    return code == 0   ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, 0, false, false, true>)
+           : code == 1 ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, 1, false, false, true>)
+                       : reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, 2, false, false, true>);
 }
 
 // code: -1 to read x, -2 to read x in rows that start anywhere.
@@ -395,17 +409,18 @@ template <typename T>
 const void *rms_grad_kernel(int nv, int code, bool full)
 {
     if (code == -2)
-        return nv == 1   ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 1, -1, true, false>)
-               : nv == 2 ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 2, -1, true, false>)
-                         : reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, -1, true, false>);
+        return nv == 1   ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 1, -1, true, false, false>)
+               : nv == 2 ? reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 2, -1, true, false, false>)
+                         : reinterpret_cast<void *>(&taco_rms_grad_kernel<T, 4, -1, true, false, false>);
     return code < 0    ? rms_grad_kernel<T, -1>(nv, full)
            : code == 0 ? rms_grad_kernel<T, 0>(nv, full)
            : code == 1 ? rms_grad_kernel<T, 1>(nv, full)
                        : rms_grad_kernel<T, 2>(nv, full);
 }
 
+// Kernel and shape; false where the rows do not fit shared memory.
 template <typename T>
-bool rms_grad_shared(RmsGradArgs *a, int sms, cudaStream_t stream, cudaError_t *result)
+bool rms_grad_shared(RmsGradArgs *a, bool direct, int sms, cudaStream_t stream, cudaError_t *result)
 {
     const int64_t C = a->hidden;
     const bool records = !a->x, odd = C % 8 != 0;
@@ -415,7 +430,7 @@ bool rms_grad_shared(RmsGradArgs *a, int sms, cudaStream_t stream, cudaError_t *
     int warps = (vectors + 32 * nv - 1) / (32 * nv);
     int groups = row_groups(a->rows, warps, kRmsGradThreads, sms);
     const size_t weight = 32 * static_cast<size_t>(vectors);
-    const size_t place = static_cast<size_t>(1 + !records + (a->dsummed != nullptr)) * nv * warps * 256 * sizeof(T) +
+    const size_t place = static_cast<size_t>(1 + !records + (!direct && a->dsummed)) * nv * warps * 256 * sizeof(T) +
                          (records ? (C / a->block * (a->block + 8) + 8 + 15) / 16 * 16 : 0);
     // fewer groups where their rows do not fit, with records three of each
     while (groups > 1 && (weight + groups * place > max_shared<T>(180) || (records && ring_stages(weight, groups * place) < 3)))
@@ -427,8 +442,9 @@ bool rms_grad_shared(RmsGradArgs *a, int sms, cudaStream_t stream, cudaError_t *
         return false;
     a->nparts = shifted_grid((a->rows + groups - 1) / groups, groups, odd, std::min(sms, kMaxColumnParts));
     void *p[] = {a, &warps, &groups, &stages};
-    *result = launch_kernel(rms_grad_kernel<T>(nv, records ? a->code : odd ? -2 : -1, C == warps * nv * 256), a->nparts,
-                            warps * groups * 32, smem, stream, p);
+    *result = launch_kernel(direct ? rms_grad_direct_kernel<T>(a->code)
+                                   : rms_grad_kernel<T>(nv, records ? a->code : odd ? -2 : -1, C == warps * nv * 256),
+                            a->nparts, warps * groups * 32, smem, stream, p);
     return true;
 }
 
@@ -436,7 +452,10 @@ template <typename T>
 cudaError_t rms_grad_any(RmsGradArgs *a, int sms, cudaStream_t stream)
 {
     cudaError_t result;
-    if (rms_grad_shared<T>(a, sms, stream, &result))
+    if (rms_grad_shared<T>(a, false, sms, stream, &result))
+        return result;
+    // (all rows that do not fit have four vectors a lane)
+    if (!a->x && a->dsummed && rms_grad_shared<T>(a, true, sms, stream, &result))
         return result;
     void *p[] = {a};
     const bool vectors = a->hidden % 8 == 0;
@@ -465,6 +484,12 @@ cudaError_t init_rms_grad_type()
                 if (e != cudaSuccess)
                     return e;
             }
+    for (int code = 0; code < 3; code++) {
+        const cudaError_t e = cudaFuncSetAttribute(rms_grad_direct_kernel<T>(code), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kMaxShared));
+        if (e != cudaSuccess)
+            return e;
+    }
     return cudaSuccess;
 }
 
