@@ -207,6 +207,9 @@ TACO_API taco_status_t taco_reduce_shards_ex(const void *const *packed_shards, i
  *     and leaves mean and rstd as they are.
  *   - Workspaces hold nothing between calls; a call that gets fewer bytes than
  *     its *_workspace() query returns TACO_ERR_BAD_SHAPE.
+ *   - The first call of the RMS norm, of the gated layer and of the other
+ *     operators on a device sets the kernels of that family up; after that they
+ *     may be captured into CUDA graphs.
  * ------------------------------------------------------------------------- */
 typedef enum taco_dtype {
     TACO_DTYPE_BF16 = 0,
