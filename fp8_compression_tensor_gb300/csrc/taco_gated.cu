@@ -11,7 +11,8 @@
 // of W and the odd one the up projection's, so one product gives both halves of
 // every element to the same thread of the epilogue, and z never leaves the chip
 // but as records.  Operands come by TMA (128-byte swizzle; x, W and dz K-major, for
-// dx W N-major) in five stages of 64 along K; all copies of a stage count on the
+// dx W N-major) in five stages of 64 along K (seven of narrow tiles, 64 columns of
+// each projection, where there are few); all copies of a stage count on the
 // even CTA's barrier.  Two accumulators of 256 tensor-memory columns take turns, so
 // the epilogue of a tile runs beside the next one's products.
 //
@@ -34,17 +35,26 @@ namespace {
 
 constexpr int kTileM = 256;                   // rows of a pair's tile
 constexpr int kStageK = 64;                   // of the sum per pipeline stage
-constexpr int kStages = 5;
-constexpr int kOperandBytes = 128 * kStageK * 2, kStageBytes = 2 * kOperandBytes;   // of one CTA
-constexpr int kHalfBytes = 64 * kStageK * 2;                                        // 64 columns of an N-major B
-// An epilogue warp's buffer for what it writes, and behind it the bias of its columns.
-constexpr int kWarpBytes = 8192, kBiasAt = 6144;                                    // one of eight, without records
-constexpr int kOutBytes = 4096 + 1024, kRecordBytes = 5120, kRecordWarpBytes = kRecordBytes + 512;   // four and eight, with records
+constexpr int kOperandBytes = 128 * kStageK * 2;      // one CTA's A of a stage
+constexpr int kHalfBytes = 64 * kStageK * 2;          // 64 columns of an N-major B
 constexpr int kThreads = 512;
-constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + 8 * kWarpBytes;
-static_assert(4 * kOutBytes + 8 * kRecordWarpBytes <= 8 * kWarpBytes, "buffers");
+
+// Shared memory of a kernel whose tiles have N columns of each projection.
+template <int N>
+struct Shape {
+    static constexpr int kStages = N == 128 ? 5 : 7;
+    static constexpr int kStageBytes = kOperandBytes + N * kStageK * 2;   // of one CTA
+    // An epilogue warp's buffer for what it writes, and behind it the bias of its columns: without records of one of up to
+    // eight warps, with them of four and eight.
+    static constexpr int kWarpBytes = N == 128 ? 8192 : 5120, kBiasAt = N == 128 ? 6144 : 4096;
+    static constexpr int kOutBytes = 4096 + 1024, kRecordBytes = 40 * N, kRecordWarpBytes = kRecordBytes + 512;
+    static constexpr int kBuffers = N == 128 ? 8 * kWarpBytes : 4 * kOutBytes + 8 * kRecordWarpBytes;
+    static_assert(4 * kOutBytes + 8 * kRecordWarpBytes <= kBuffers, "buffers");
+    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kBuffers;
+};
 constexpr int kInputGrad = -1;                // in the place of an activation: dx = dz W
 
+template <int kStages>
 struct Barriers {
     uint64_t full[kStages];       // even CTA: both CTAs' A and B of the stage have landed
     uint64_t empty[kStages];      // the stage's products are done
@@ -203,8 +213,9 @@ __device__ __forceinline__ void encode_row32(const float (&z)[32], float inv, ui
     }
 }
 
-// Records of 128 columns of one projection (k: 0 gate, 1 up) from column c on, 32
+// Records of N columns of one projection (k: 0 gate, 1 up) from column c on, 32
 // rows from `row` on; `acc` the first column's accumulators, `bias` its staged bias.
+// (N: columns of the tile, 128 or, for blocks up to 64, 64.)
 // A block's accumulators are read twice, for its maximum and for its codes.  The
 // rows' record bytes go through the buffer (at an odd number of eight bytes apart,
 // which the banks like, but for blocks of 32, which fill it) and out in row order.
@@ -212,12 +223,13 @@ __device__ __forceinline__ void encode_row32(const float (&z)[32], float inv, ui
 // through the buffers is what an epilogue costs: of 8192 x 1024 x 4096 y takes 4 us
 // and the records 14, of 70 without either.  16 bytes a lane on the way out took as
 // long.
+template <int N>
 __device__ __forceinline__ void write_tile_records(uint32_t acc, uint32_t bias, uint32_t buffer, const TileArgs &a, int k, int64_t row,
                                                    int64_t c)
 {
     const int lane = threadIdx.x & 31, shift = 31 - __clz(a.block), block = a.block;
-    const int cols = static_cast<int>(a.width - c < 128 ? a.width - c : 128);
-    const uint32_t pitch = block == 32 ? 160 : (16 + (128 >> shift) | 1) * 8;
+    const int cols = static_cast<int>(a.width - c < N ? a.width - c : N);
+    const uint32_t pitch = block == 32 ? N + N / 4 : (N / 8 + (N >> shift) | 1) * 8;
     uint32_t to = buffer + lane * pitch;
 #pragma unroll 1
     for (int b = 0; b < cols; b += block) {
@@ -263,13 +275,16 @@ __device__ __forceinline__ void write_tile_records(uint32_t acc, uint32_t bias, 
     __syncwarp();
 }
 
-template <int ACT>
+// N: columns of each projection in a tile (of dx half of its columns).
+template <int ACT, int N>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_out, TileArgs a, Plan plan, uint32_t idesc, uint32_t *fault)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) Barriers bars;
+    using S = Shape<N>;
+    constexpr int kStages = S::kStages, kStageBytes = S::kStageBytes;
+    __shared__ __align__(8) Barriers<kStages> bars;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -284,7 +299,7 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(bar(bars.acc_full[b]), 1);
-            mbar_init(bar(bars.acc_empty[b]), a.packed ? 24 : 16);   // the epilogue warps of both CTAs
+            mbar_init(bar(bars.acc_empty[b]), a.packed ? 24 : N == 128 ? 16 : 8);   // the epilogue warps of both CTAs
         }
         mbar_init(bar(bars.drained), 1);
         fence_mbar_init();
@@ -327,7 +342,7 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     pair_load_2d(dst + kOperandBytes, &map_b, col, k * kStageK, full);
                     pair_load_2d(dst + kOperandBytes + kHalfBytes, &map_b, col + 64, k * kStageK, full);
                 } else {
-                    pair_load_2d(dst + kOperandBytes, &map_b, k * kStageK, n * 128 + (rank ? static_cast<int>(a.width) : 0), full);
+                    pair_load_2d(dst + kOperandBytes, &map_b, k * kStageK, n * N + (rank ? static_cast<int>(a.width) : 0), full);
                 }
                 used |= 1u << s;
                 if (++s == kStages) {
@@ -381,15 +396,15 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             own_commit(bar(bars.drained));
             mbar_wait_bounded_thread(bar(bars.drained), 0, fault, kFaultGated);
         }
-    } else if (warp >= 4 && (warp < 12 || a.packed)) {
+    } else if (warp >= 4 && (warp < (N == 128 ? 12 : 8) || a.packed)) {
         const int quarter = warp & 3, team = (warp - 4) >> 2;
         const bool records = ACT != kInputGrad && a.packed;
         const bool out = !records || team == 0;                   // writes y or dx, not records
         const uint32_t empty0 = in_even_cta(bar(bars.acc_empty[0])), buffers = base + kStages * kStageBytes;
-        const uint32_t buffer = !records ? buffers + (warp - 4) * kWarpBytes
-                                : out    ? buffers + quarter * kOutBytes
-                                         : buffers + 4 * kOutBytes + (warp - 8) * kRecordWarpBytes;
-        const uint32_t bias = buffer + (!records ? kBiasAt : out ? 4096 : kRecordBytes);
+        const uint32_t buffer = !records ? buffers + (warp - 4) * S::kWarpBytes
+                                : out    ? buffers + quarter * S::kOutBytes
+                                         : buffers + 4 * S::kOutBytes + (warp - 8) * S::kRecordWarpBytes;
+        const uint32_t bias = buffer + (!records ? S::kBiasAt : out ? 4096 : S::kRecordBytes);
         uint32_t turn = 0;
         for (int64_t u = first_unit; u < plan.units; u += step_units, turn++) {
             int m, n, first, count;
@@ -397,9 +412,9 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             plan.at(u, m, n, part, first, count);
             const uint32_t b = turn & 1u;
             if (ACT != kInputGrad && a.bias) {
-                stage_bias(bias, a, out ? 0 : team - 1, static_cast<int64_t>(n) * 128);
+                stage_bias(bias, a, out ? 0 : team - 1, static_cast<int64_t>(n) * N);
                 if (out)
-                    stage_bias(bias + 512, a, 1, static_cast<int64_t>(n) * 128);
+                    stage_bias(bias + 512, a, 1, static_cast<int64_t>(n) * N);
                 __syncwarp();
             }
             if (!mbar_wait_bounded(bar(bars.acc_full[b]), (turn >> 1) & 1u, fault, kFaultGated))
@@ -443,8 +458,8 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     write_staged(place, &map_out, a, row, static_cast<int64_t>(n) * 256 + team * 128 + c * 64);
                 }
             } else if (out) {
-                const int64_t c0 = static_cast<int64_t>(n) * 128;
-                const int begin = records ? 0 : team * 64, end = records ? 128 : begin + 64;
+                const int64_t c0 = static_cast<int64_t>(n) * N;
+                const int begin = records ? 0 : team * 64, end = records ? N : begin + 64;
 #pragma unroll 1
                 for (int c = begin; c < end; c += 32) {
                     if (c % 64 == 0) {
@@ -453,7 +468,7 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     }
                     uint32_t rg[32], ru[32];
                     tmem_ld32(acc + c, rg);
-                    tmem_ld32(acc + 128 + c, ru);
+                    tmem_ld32(acc + N + c, ru);
                     tmem_ld_wait();
                     float g[32], v[32];
                     to_z(rg, a, bias + c * 4, g);
@@ -469,7 +484,7 @@ taco_gated_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                         write_staged(buffer, &map_out, a, row, c0 + c - 32);
                 }
             } else {
-                write_tile_records(acc + (team - 1) * 128, bias, buffer, a, team - 1, row, static_cast<int64_t>(n) * 128);
+                write_tile_records<N>(acc + (team - 1) * N, bias, buffer, a, team - 1, row, static_cast<int64_t>(n) * N);
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -510,20 +525,28 @@ __global__ void __launch_bounds__(256) taco_gated_join_kernel(TileArgs a, Plan p
     }
 }
 
+template <int N>
 const void *kernel_of(int activation)
 {
-    return activation == kSilu       ? reinterpret_cast<void *>(&taco_gated_kernel<kSilu>)
-           : activation == kGelu     ? reinterpret_cast<void *>(&taco_gated_kernel<kGelu>)
-           : activation == kGeluTanh ? reinterpret_cast<void *>(&taco_gated_kernel<kGeluTanh>)
-                                     : reinterpret_cast<void *>(&taco_gated_kernel<kInputGrad>);
+    return activation == kSilu   ? reinterpret_cast<void *>(&taco_gated_kernel<kSilu, N>)
+           : activation == kGelu ? reinterpret_cast<void *>(&taco_gated_kernel<kGelu, N>)
+                                 : reinterpret_cast<void *>(&taco_gated_kernel<kGeluTanh, N>);
 }
 
-cudaError_t launch_pairs(const void *fn, int pairs, cudaStream_t stream, void **args)
+// narrow: 64 columns a tile.
+const void *kernel_of(int activation, bool narrow)
+{
+    return activation == kInputGrad ? reinterpret_cast<void *>(&taco_gated_kernel<kInputGrad, 128>)
+           : narrow                 ? kernel_of<64>(activation)
+                                    : kernel_of<128>(activation);
+}
+
+cudaError_t launch_pairs(const void *fn, size_t smem, int pairs, cudaStream_t stream, void **args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -541,15 +564,19 @@ int group_of(int64_t tiles_m, int64_t K)
 
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 
-constexpr uint32_t kDescF16 = mma_idesc_f16_f32(256, 256), kDescBf16 = mma_idesc_bf16_f32(256, 256);
+// The pairs of a GB300, not of the current device: the workspace query that shares
+// the plan of dx looks at none.  With another count the plan is only less even.
+constexpr int64_t kPairs = 76;
 
 }  // namespace
 
 cudaError_t init_gated()
 {
     cudaError_t e = cudaSuccess;
-    for (int act = kInputGrad; act <= kGeluTanh && e == cudaSuccess; act++)
-        e = cudaFuncSetAttribute(kernel_of(act), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    for (int act = kInputGrad; act <= kGeluTanh; act++)
+        for (int narrow = 0; narrow < (act == kInputGrad ? 1 : 2) && e == cudaSuccess; narrow++)
+            e = cudaFuncSetAttribute(kernel_of(act, narrow), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(narrow ? Shape<64>::kSmem : Shape<128>::kSmem));
     return e == cudaSuccess ? init_gated_serve() : e;
 }
 
@@ -583,25 +610,32 @@ cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStrea
     const CUtensorMapDataType type = a.dtype == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     alignas(64) CUtensorMap map_x, map_w, map_y = {};
     const bool tma_out = a.inner % 8 == 0;
+    // 64 columns a tile where these fit one wave of the pairs, which 128 fill half at most.  A stage then takes 0.23 us (the
+    // rate at which an SM's 24 KB come from L2) against 0.28 (its products), in seven stages instead of five, and an
+    // epilogue half as long: 256 x 4096 x 3584 20.0 us against 24.4, 512 x 8192 x 2048 34.4 against 41.7.
+    const int64_t tiles_m = (a.rows + kTileM - 1) / kTileM;
+    const bool narrow = tiles_m * ((a.inner + 63) / 64) <= kPairs && !(a.packed && a.block > 64);
+    const int columns = narrow ? 64 : 128;
     if (e == cudaSuccess)
         e = encode_2d(&map_x, type, x, a.hidden, a.rows, 2 * pitch, kStageK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess)
-        e = encode_2d(&map_w, type, w, a.hidden, 2 * a.inner, 2 * pitch, kStageK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+        e = encode_2d(&map_w, type, w, a.hidden, 2 * a.inner, 2 * pitch, kStageK, columns, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess && tma_out)
         e = encode_2d(&map_y, type, a.y, a.inner, a.rows, 2 * a.inner, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess)
         return e;
     Plan plan = {};
-    plan.tiles_m = static_cast<int>((a.rows + kTileM - 1) / kTileM);
-    plan.tiles_n = static_cast<int>((a.inner + 127) / 128);
+    plan.tiles_m = static_cast<int>(tiles_m);
+    plan.tiles_n = static_cast<int>((a.inner + columns - 1) / columns);
     plan.group_m = group_of(plan.tiles_m, a.hidden);
     plan.stages_total = static_cast<int>((a.hidden + kStageK - 1) / kStageK);
     plan.whole = plan.units = static_cast<int64_t>(plan.tiles_m) * plan.tiles_n;
     plan.splits = 1;
     TileArgs args{a.y, a.packed, a.bias, nullptr, a.rows, a.inner, a.param_dtype, a.block, a.code, a.dtype == kTypeF16, tma_out};
-    uint32_t idesc = a.dtype == kTypeF16 ? kDescF16 : kDescBf16;
+    uint32_t idesc = a.dtype == kTypeF16 ? mma_idesc_f16_f32(256, 2 * columns) : mma_idesc_bf16_f32(256, 2 * columns);
     void *p[] = {&map_x, &map_w, &map_y, &args, &plan, &idesc, &fault};
-    return launch_pairs(kernel_of(a.activation), static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
+    return launch_pairs(kernel_of(a.activation, narrow), narrow ? Shape<64>::kSmem : Shape<128>::kSmem,
+                        static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
 }
 
 // Tiles of dx, how many at the end are cut into ranges of K, and into how many.
@@ -613,10 +647,6 @@ cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStrea
 // tiles) 77 in two and 99 whole; 8192 x 4096 x 16384 (56 tiles in the last wave of
 // 7) and 640 x 5120 x 13824 (60 tiles) would take 1411 and 154 cut, 1416 and 146
 // whole.
-// The pairs of a GB300, not of the current device: the workspace query that shares
-// the plan looks at none.  With another count the plan is only less even.
-constexpr int64_t kPairs = 76;
-
 struct Split {
     int64_t tiles, tail, splits;
 };
@@ -679,9 +709,10 @@ cudaError_t launch_gated_input_grad(const GatedInputGradArgs &a, uint32_t *fault
     plan.whole = s.tiles - s.tail;
     plan.units = plan.whole + s.tail * s.splits;
     TileArgs args{a.dx, nullptr, nullptr, static_cast<float *>(a.workspace), a.rows, a.hidden, 0, 0, 0, a.dtype == kTypeF16, tma_out};
-    uint32_t idesc = (a.dtype == kTypeF16 ? kDescF16 : kDescBf16) | (1u << 16);   // B N-major
+    uint32_t idesc = (a.dtype == kTypeF16 ? mma_idesc_f16_f32(256, 256) : mma_idesc_bf16_f32(256, 256)) | (1u << 16);   // B N-major
     void *p[] = {&map_dz, &map_w, &map_dx, &args, &plan, &idesc, &fault};
-    e = launch_pairs(kernel_of(kInputGrad), static_cast<int>(std::min<int64_t>(plan.units, sms / 2)), stream, p);
+    e = launch_pairs(kernel_of(kInputGrad, false), Shape<128>::kSmem, static_cast<int>(std::min<int64_t>(plan.units, sms / 2)),
+                     stream, p);
     if (e == cudaSuccess && plan.tail > 0) {
         void *q[] = {&args, &plan};
         e = launch_kernel(reinterpret_cast<void *>(&taco_gated_join_kernel),

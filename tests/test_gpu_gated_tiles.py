@@ -55,3 +55,19 @@ def test_few_rows_in_clusters(taco):  # noqa: F811
     """Every number of CTAs a cluster: 1 to 8 along K."""
     for inner in (30 * 64, 38 * 64, 45 * 64, 54 * 64, 68 * 64, 90 * 64, 136 * 64, 137 * 64, 280 * 64):
         check_forward(taco, 5, 2072, inner, F16, "gelu")
+
+
+@pytest.mark.parametrize("rows,inner", [(200, 64), (200, 65), (300, 2432), (300, 2433), (300, 2400), (700, 1600), (2000, 576), (2000, 608),
+                                        (256, 4864), (256, 4872), (257, 4864)])
+@pytest.mark.parametrize("dtype,block", [(BF16, None), (F16, 64), (BF16, 32), (BF16, 128)])
+def test_narrow_tiles(taco, rows, inner, dtype, block):  # noqa: F811
+    """Both sides of the number of tiles up to which they are 64 columns wide."""
+    if block is None or inner % block == 0:
+        check_forward(taco, rows, 200, inner, dtype, "silu", F32 if rows % 3 else None, block, "e4m3" if rows % 7 else "int8")
+
+
+def test_narrow_and_wide_tiles_agree(taco):  # noqa: F811
+    """Either width adds the same products in the same order: records of blocks of 64 (narrow) and 128 (wide) aside, y is the same."""
+    x, w = values(1, 300, 1000).to(BF16).cuda(), (values(2, 2 * 1280, 1000) / 32).to(BF16).cuda()
+    narrow, wide = taco.gated_linear(x, w, checkpoint=True, block=64), taco.gated_linear(x, w, checkpoint=True, block=128)
+    assert torch.equal(narrow.y, wide.y)
