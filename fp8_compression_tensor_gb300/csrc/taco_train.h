@@ -93,6 +93,14 @@ struct GatedGradArgs {
     int activation, block, code, nparts;
 };
 
+// Column sums that launch_column_sums would make of one array (parts null: none).
+struct ColumnSums {
+    const float *parts;
+    int64_t n;
+    void *out;
+    int nparts, dtype;
+};
+
 // dx = dz W
 struct GatedInputGradArgs {
     const void *dz, *weight;
@@ -157,7 +165,8 @@ cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStrea
 cudaError_t init_gated_serve();
 bool gated_serves(int64_t rows, int64_t inner);
 cudaError_t launch_gated_serve(const GatedArgs &a, const void *x, const void *w, int64_t pitch, uint32_t *fault, int sms, cudaStream_t stream);
-cudaError_t launch_gated_input_grad(const GatedInputGradArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
+// `sums` are made behind the product, in the same launch as the joining of its parts where there are some.
+cudaError_t launch_gated_input_grad(const GatedInputGradArgs &a, const ColumnSums &sums, uint32_t *fault, int sms, cudaStream_t stream);
 
 // Workspace of a weight gradient and the range its kernels address.
 int64_t weight_grad_workspace(int64_t rows, int64_t out, int64_t hidden);

@@ -553,10 +553,10 @@ taco_status_t taco_gated_linear_backward(const taco_gated_linear_backward_args_t
         e = launch_gated_grad(a->dtype, &k, dev->sm_count, s);
     if (e == cudaSuccess && a->rows != 0 && a->dx) {
         const GatedInputGradArgs g{a->dz, a->weight, a->dx, a->workspace, a->rows, a->inner, a->hidden, a->dtype};
-        e = launch_gated_input_grad(g, dev->fault, dev->sm_count, s);
-    }
-    if (e == cudaSuccess && a->dbias)
+        e = launch_gated_input_grad(g, ColumnSums{parts, 2 * a->inner, a->dbias, k.nparts, a->param_dtype}, dev->fault, dev->sm_count, s);
+    } else if (e == cudaSuccess && a->dbias) {
         e = launch_column_sums(parts, k.nparts, 2 * a->inner, a->dbias, nullptr, a->param_dtype, s);
+    }
     return done(e);
 }
 
