@@ -8,9 +8,9 @@
 // of the grid, which is a multiple of 8 (or takes one row a group), so its rows
 // have one shift: parameters are staged shifted once, and a thread keeps its
 // columns from row to row, which the column sums of a gradient need.  Odd widths
-// then cost the edges' masks and stores alone: 8192 x 4097 bf16 with a residual
-// takes as long as the rows' bytes do, where copies to shared memory that are read
-// 32 columns apart (the layer norm's way) take 73 us.
+// then cost what their edges do: 8192 x 4097 bf16 with a residual takes 47 us and
+// 8192 x 4096 45, where copies to shared memory that are read 32 columns apart (the
+// layer norm's way) take 73.
 #pragma once
 
 #include "taco_norm.cuh"
@@ -18,7 +18,7 @@
 namespace taco {
 namespace {
 
-// The first of the row's columns in the group's vector v, and whether the vector reaches outside the row.
+// Whether a vector whose first column is c reaches outside the row.
 __device__ __forceinline__ bool at_edge(int c, int C) { return c < 0 || c + 8 > C; }
 
 // Zeros for what lies outside the row in `tensors` pieces of a vector whose first column is c, `pitch` bytes apart and
@@ -77,7 +77,7 @@ __device__ __forceinline__ F8 load_param_edge(const void *p, int dtype, int c, i
     return F8{{make_float2(f[0], f[1]), make_float2(f[2], f[3]), make_float2(f[4], f[5]), make_float2(f[6], f[7])}};
 }
 
-// Vectors of a row of any shift, and the shared memory of its parameters in planes (taco_norm.cuh), shifted.
+// Vectors of a row of any shift.
 __host__ __device__ constexpr int row_vectors(int64_t hidden) { return static_cast<int>(hidden % 8 ? (hidden + 14) / 8 : hidden / 8); }
 
 // Stages a parameter array in planes of `vectors` vectors, vector v from column 8 v - shift on.
