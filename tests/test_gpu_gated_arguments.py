@@ -95,3 +95,34 @@ def test_threads(taco):  # noqa: F811
     for t in threads:
         t.join()
     assert not failed
+
+
+@pytest.mark.parametrize("rows", (40, 300))
+def test_padding_rows(taco, rows):  # noqa: F811
+    """Rows of zeros (padding) give zeros: all-zero records with s = 0, and no gradient from them."""
+    x, w = values(1, rows, 136).to(BF16).cuda(), (values(2, 512, 136) / 12).to(BF16).cuda()
+    x[5:17] = 0
+    f = taco.gated_linear(x, w, checkpoint=True)
+    assert not f.y[5:17].any() and not taco.gated_linear(x, w).y[5:17].any()
+    records = f.packed.view(rows, 4, 136)[5:17]
+    assert not records[:, :, :128].any() and not records[:, :, 132:].any()
+    assert torch.all(records[:, :, 128:132].contiguous().view(torch.float32) == 1)
+    g = taco.gated_linear_backward(values(3, rows, 256).to(BF16).cuda(), f.packed, w, recompute=True)
+    assert not g.dz[5:17].any() and not g.dx[5:17].any() and not g.y[5:17].any()
+    n = taco.rmsnorm(x, checkpoint=False)
+    assert not n.y[5:17].any() and torch.isfinite(n.rstd).all()
+    assert torch.isfinite(taco.rmsnorm_backward(x, n.rstd, x=x).dx).all()
+
+
+@pytest.mark.parametrize("rows", (3, 200))
+def test_products_beyond_binary32(taco, rows):  # noqa: F811
+    """Projections that overflow are infinite: their blocks decode to NaN, other rows and blocks stay."""
+    x, w = values(1, rows, 64).to(BF16), values(2, 512, 64).to(BF16)
+    clean = taco.gated_linear(x.cuda(), w.cuda(), checkpoint=True)
+    x[2] = 1e30
+    w[130] = 3e38        # gate column 130: the second block of the gate
+    got = taco.gated_linear(x.cuda(), w.cuda(), checkpoint=True)
+    v, want = (taco.decompress(r.packed, rows, 512, variant="ds_only") for r in (got, clean))
+    assert torch.isnan(v[2, 128:256]).all() and torch.isfinite(v[2, :128]).all() and torch.isfinite(v[2, 256:]).all()
+    keep = torch.arange(rows, device="cuda") != 2
+    assert torch.equal(v[keep][:, :128], want[keep][:, :128]) and torch.equal(v[keep][:, 256:], want[keep][:, 256:])
