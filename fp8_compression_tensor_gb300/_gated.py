@@ -20,7 +20,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _training
-from ._binding import _check
+from ._binding import _check, _raw_stream
 from ._training import (DTYPES, _address, _code, _f32, _first, _i32, _i64, _packed, _packer, _param_type, _ptr, _record_bytes,
                         _run, _tensor, _workspace_bytes)
 
@@ -75,6 +75,18 @@ def _library() -> ctypes.CDLL:
     return _lib
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(device: int, stream, call, *args):
+    """call(handle, *args) on the device and the stream (_training._run).  On the
+    current ones it is called directly: a closure and the look for a device
+    cost two of the fifteen microseconds of a small call."""
+    if stream is None and _raw_stream is not None and device == _current_device():
+        return call(_raw_stream(device), *args)
+    return _run(device, stream, lambda handle: call(handle, *args))
+
+
 class RmsNorm(NamedTuple):
     y: torch.Tensor
     rstd: torch.Tensor
@@ -115,25 +127,26 @@ def rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float =
     pr = _tensor(residual, "residual", device, x.dtype, shape)
     pw = _tensor(weight, "weight", device, pdtype, (hidden,))
     nbytes = _record_bytes(rows, hidden, block) if checkpoint or packed_y else 0
-    lib = _library()
-
-    def call(handle):
-        y = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if packed_y else torch.empty_like(x)
-        summed = torch.empty_like(x) if residual is not None else None
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
-        if hidden == 0:   # no element to average: 0 / 0 (the library launches nothing)
-            rstd.fill_(math.nan)
-        packed = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if checkpoint else None
-        py = y.data_ptr()
-        rc = lib.taco_rmsnorm(
-            _pack_rmsnorm(x.data_ptr(), pr, pw, 0 if packed_y else py, _address(summed), rstd.data_ptr(), _address(packed),
-                          py if packed_y else 0, rows, hidden, eps, kind, DTYPES[pdtype], block, _code(code)), handle)
-        return rc, RmsNorm(y, rstd, summed, packed)
-
-    rc, result = _run(device, stream, call)
+    rc, result = _launch(device, stream, _rmsnorm, x, pw, eps, residual is not None, pr, checkpoint, packed_y, nbytes, rows,
+                         hidden, kind, DTYPES[pdtype], block, _code(code))
     if rc:
         _check(rc, "taco_rmsnorm")
     return result
+
+
+def _rmsnorm(handle, x, weight, eps, add, residual, checkpoint, packed_y, nbytes, rows, hidden, kind, pkind, block, code):
+    device = x.device
+    y = torch.empty(nbytes, dtype=torch.uint8, device=device) if packed_y else torch.empty_like(x)
+    summed = torch.empty_like(x) if add else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+    if hidden == 0:   # no element to average: 0 / 0 (the library launches nothing)
+        rstd.fill_(math.nan)
+    packed = torch.empty(nbytes, dtype=torch.uint8, device=device) if checkpoint else None
+    py = y.data_ptr()
+    rc = _library().taco_rmsnorm(
+        _pack_rmsnorm(x.data_ptr(), residual, weight, 0 if packed_y else py, _address(summed), rstd.data_ptr(), _address(packed),
+                      py if packed_y else 0, rows, hidden, eps, kind, pkind, block, code), handle)
+    return rc, RmsNorm(y, rstd, summed, packed)
 
 
 def rmsnorm_backward(dy: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -153,25 +166,26 @@ def rmsnorm_backward(dy: torch.Tensor, rstd: torch.Tensor, weight: Optional[torc
     ppacked = 0 if packed is None else _packed(packed, rows, hidden, block, device)
     pw = _tensor(weight, "weight", device, pdtype, (hidden,))
     pds = _tensor(dsummed, "dsummed", device, dy.dtype, shape)
-    lib = _library()
-
-    def call(handle):
-        dx = torch.empty_like(dy)
-        dweight = ws = None
-        nbytes = 0
-        if weight is not None:
-            dweight = torch.empty_like(weight)
-            nbytes = _workspace_bytes("taco_rmsnorm_backward_workspace", rows, hidden)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
-        rc = lib.taco_rmsnorm_backward(
-            _pack_rmsnorm_backward(dy.data_ptr(), px, prstd, ppacked, pw, pds, dx.data_ptr(), _address(dweight), _address(ws),
-                                   nbytes, rows, hidden, kind, DTYPES[pdtype], block, _code(code)), handle)
-        return rc, RmsNormGrads(dx, dweight)
-
-    rc, result = _run(device, stream, call)
+    rc, result = _launch(device, stream, _rmsnorm_backward, dy, px, prstd, ppacked, weight, pw, pds, rows, hidden, kind,
+                         DTYPES[pdtype], block, _code(code))
     if rc:
         _check(rc, "taco_rmsnorm_backward")
     return result
+
+
+def _rmsnorm_backward(handle, dy, x, rstd, packed, weight, pweight, dsummed, rows, hidden, kind, pkind, block, code):
+    lib = _library()
+    dx = torch.empty_like(dy)
+    dweight = ws = None
+    nbytes = 0
+    if weight is not None:
+        dweight = torch.empty_like(weight)
+        nbytes = _workspace_bytes("taco_rmsnorm_backward_workspace", rows, hidden)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
+    rc = lib.taco_rmsnorm_backward(
+        _pack_rmsnorm_backward(dy.data_ptr(), x, rstd, packed, pweight, dsummed, dx.data_ptr(), _address(dweight), _address(ws),
+                               nbytes, rows, hidden, kind, pkind, block, code), handle)
+    return rc, RmsNormGrads(dx, dweight)
 
 
 def _activation(name: str) -> int:
@@ -213,22 +227,23 @@ def gated_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     if hidden == 0:
         raise ValueError("x must have at least one column")
     nbytes = _record_bytes(rows, 2 * inner, block) if checkpoint else 0
-    lib = _library()
-
-    def call(handle):
-        y = torch.empty((*x.shape[:-1], inner), dtype=x.dtype, device=x.device)
-        packed = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if checkpoint else None
-        wbytes = _workspace_bytes("taco_gated_linear_workspace", rows, inner, hidden)
-        ws = torch.empty(wbytes, dtype=torch.uint8, device=x.device) if wbytes > 0 else None
-        rc = lib.taco_gated_linear(
-            _pack_gated(x.data_ptr(), pw, pb, y.data_ptr(), _address(packed), _address(ws), wbytes, rows, inner, hidden, kind,
-                        DTYPES[pdtype], act, block, _code(code)), handle)
-        return rc, GatedLinear(y, packed)
-
-    rc, result = _run(device, stream, call)
+    rc, result = _launch(device, stream, _gated_linear, x, pw, pb, checkpoint, nbytes, rows, inner, hidden, kind, DTYPES[pdtype],
+                         act, block, _code(code))
     if rc:
         _check(rc, "taco_gated_linear")
     return result
+
+
+def _gated_linear(handle, x, weight, bias, checkpoint, nbytes, rows, inner, hidden, kind, pkind, activation, block, code):
+    lib, device = _library(), x.device
+    y = torch.empty((*x.shape[:-1], inner), dtype=x.dtype, device=device)
+    packed = torch.empty(nbytes, dtype=torch.uint8, device=device) if checkpoint else None
+    wbytes = _workspace_bytes("taco_gated_linear_workspace", rows, inner, hidden)
+    ws = torch.empty(wbytes, dtype=torch.uint8, device=device) if wbytes > 0 else None
+    rc = lib.taco_gated_linear(
+        _pack_gated(x.data_ptr(), weight, bias, y.data_ptr(), _address(packed), _address(ws), wbytes, rows, inner, hidden, kind,
+                    pkind, activation, block, code), handle)
+    return rc, GatedLinear(y, packed)
 
 
 def gated_linear_backward(dy: torch.Tensor, packed: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -254,25 +269,26 @@ def gated_linear_backward(dy: torch.Tensor, packed: torch.Tensor, weight: Option
         if hidden == 0:
             raise ValueError("weight must have at least one column")
         pw = _tensor(weight, "weight", device, dy.dtype, (2 * inner, hidden))
-    lib = _library()
-
-    def call(handle):
-        lead = dy.shape[:-1]
-        dz = torch.empty((*lead, 2 * inner), dtype=dy.dtype, device=dy.device)
-        dx = torch.empty((*lead, hidden), dtype=dy.dtype, device=dy.device) if weight is not None else None
-        y = torch.empty_like(dy) if recompute else None
-        dbias = torch.empty(2 * inner, dtype=bias_dtype, device=dy.device) if bias_dtype is not None else None
-        nbytes = _workspace_bytes("taco_gated_linear_backward_workspace", rows, inner, hidden)
-        if bias_dtype is None:   # without the bias gradient's part
-            nbytes -= _workspace_bytes("taco_gated_linear_backward_workspace", rows, inner, 0)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes > 0 else None
-        rc = lib.taco_gated_linear_backward(
-            _pack_gated_backward(dy.data_ptr(), ppacked, pw, dz.data_ptr(), _address(dx), _address(y), _address(dbias),
-                                 _address(ws), nbytes, rows, inner, hidden, kind, DTYPES[bias_dtype or torch.float32], act,
-                                 block, _code(code)), handle)
-        return rc, GatedLinearGrads(dz, dx, dbias, y)
-
-    rc, result = _run(device, stream, call)
+    rc, result = _launch(device, stream, _gated_linear_backward, dy, ppacked, weight is not None, pw, bias_dtype, recompute, rows,
+                         inner, hidden, kind, act, block, _code(code))
     if rc:
         _check(rc, "taco_gated_linear_backward")
     return result
+
+
+def _gated_linear_backward(handle, dy, packed, input_grad, weight, bias_dtype, recompute, rows, inner, hidden, kind, activation,
+                           block, code):
+    lib, device, lead = _library(), dy.device, dy.shape[:-1]
+    dz = torch.empty((*lead, 2 * inner), dtype=dy.dtype, device=device)
+    dx = torch.empty((*lead, hidden), dtype=dy.dtype, device=device) if input_grad else None
+    y = torch.empty_like(dy) if recompute else None
+    dbias = torch.empty(2 * inner, dtype=bias_dtype, device=device) if bias_dtype is not None else None
+    nbytes = _workspace_bytes("taco_gated_linear_backward_workspace", rows, inner, hidden)
+    if bias_dtype is None:   # without the bias gradient's part
+        nbytes -= _workspace_bytes("taco_gated_linear_backward_workspace", rows, inner, 0)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
+    rc = lib.taco_gated_linear_backward(
+        _pack_gated_backward(dy.data_ptr(), packed, weight, dz.data_ptr(), _address(dx), _address(y), _address(dbias), _address(ws),
+                             nbytes, rows, inner, hidden, kind, DTYPES[bias_dtype or torch.float32], activation, block, code),
+        handle)
+    return rc, GatedLinearGrads(dz, dx, dbias, y)

@@ -156,6 +156,9 @@ def _tensor(t, name: str, device: int, dtype, shape) -> int:
     """Checks one more tensor and returns its address (0 for None)."""
     if t is None:
         return 0
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
