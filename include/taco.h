@@ -383,7 +383,8 @@ TACO_API taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t 
  * gate's and the others the up projection's,
  *   y = act(z_gate) z_up,  and the records of z, [rows, 2 inner] (inner % block == 0
  * then, blocks 32, 64 and 128).  The activation: silu(g) = g / (1 + exp(-g)),
- * or GELU in either form.  bf16 and f16; x and W have one type.
+ * +infinity for g = +infinity and NaN for -infinity as GELU's is, or GELU in either
+ * form.  bf16 and f16; x and W have one type.
  * 1 <= hidden < 2^31 - 256, rows < 2^31 - 256, inner < 2^30 - 256
  * (TACO_ERR_BAD_SHAPE).  rows == 0 or inner == 0 launches nothing.  Rows of x and W
  * whose hidden is no multiple of 8 are first copied to the workspace.
