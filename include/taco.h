@@ -334,6 +334,10 @@ TACO_API taco_status_t taco_weight_grad(const taco_weight_grad_args_t *args, tac
  * y is a tensor, or 8-bit records (packed_y) made from the binary32 values, for a
  * y that is sent or stored.  packed holds the records of xhat, the checkpoint
  * of the calls below.
+ * Any finite row has its norm, also one whose squares leave binary32 (their sum is
+ * then taken of scaled values), as long as rstd does not.  A row with an infinity
+ * and no NaN has rstd 0: y is NaN at the infinities and zero elsewhere.  A row of
+ * zeros has y zero, but with eps = 0 rstd infinite and y NaN.
  */
 typedef struct taco_rmsnorm_args {
     const void *x;              /* in:  [rows, hidden] */
@@ -356,7 +360,9 @@ TACO_API taco_status_t taco_rmsnorm(const taco_rmsnorm_args_t *args, taco_stream
  * Gradients of the RMS norm, with a = dy weight and c = sum a xhat / hidden:
  * dx = rstd (a - xhat c) + dsummed, dweight = sum over rows of dy xhat.  xhat
  * comes from x (what was normalised: the forward call's `summed` where it had a
- * residual) as x rstd, or from the records of the forward call.
+ * residual) as x rstd, or from the records of the forward call.  From x, the sum of
+ * a x and the products dy rstd and c rstd are binary32's: rows of up to 2^100 or
+ * down to 2^-100 are exact to its roundings with gradients between 2^-20 and 2^20.
  */
 typedef struct taco_rmsnorm_backward_args {
     const void *dy;             /* in:  [rows, hidden] */
