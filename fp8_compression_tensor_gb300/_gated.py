@@ -211,8 +211,8 @@ def _halves(features: int, name: str) -> int:
 
 def gated_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, activation: str = "silu",
                  checkpoint: bool = False, block: int = 128, code="e4m3", stream=None) -> GatedLinear:
-    """act(x Wg^T + bg) * (x Wu^T + bu) for x [..., hidden] (bf16 or f16) and
-    weight [2 inner, hidden] of x's type, the gate's rows Wg before the up
+    """act(x Wg^T + bg) * (x Wu^T + bu) for x [..., hidden] (bf16 or f16, hidden
+    up to 2^24) and weight [2 inner, hidden] of x's type, the gate's rows Wg before the up
     projection's Wu; bias [2 inner].  The activation is "silu", "gelu" or
     "gelu_tanh".  With checkpoint, `packed` holds both projections' float32
     values [..., 2 inner] as records (blocks 32, 64 and 128)."""

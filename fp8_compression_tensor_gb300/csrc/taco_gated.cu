@@ -607,6 +607,10 @@ bool gated_in_range(int64_t rows, int64_t inner, int64_t hidden)
     return rows <= INT32_MAX - 256 && inner <= INT32_MAX / 2 - 256 && hidden <= INT32_MAX - 256;
 }
 
+// The epilogue waits for all of a tile's sum at once, for kWaitLimitNs at most.  This many terms take 73 ms at 0.28 us a
+// stage of 64, so a launch has time for fourteen times that.
+bool gated_sum_in_range(int64_t terms) { return terms <= 1 << 24; }
+
 // x and W in rows of whole 16 bytes where they have others.
 int64_t gated_workspace(int64_t rows, int64_t inner, int64_t hidden)
 {

@@ -160,6 +160,7 @@ cudaError_t launch_gated_grad(int dtype, GatedGradArgs *a, int sms, cudaStream_t
 int64_t gated_workspace(int64_t rows, int64_t inner, int64_t hidden);
 int64_t gated_input_grad_workspace(int64_t rows, int64_t inner, int64_t hidden);
 bool gated_in_range(int64_t rows, int64_t inner, int64_t hidden);
+bool gated_sum_in_range(int64_t terms);   // of a product: hidden for the layer, 2 inner for dx
 cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStream_t stream);
 // The layer of few rows; x and w with rows `pitch` elements apart.
 cudaError_t init_gated_serve();

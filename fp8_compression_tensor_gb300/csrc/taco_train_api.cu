@@ -457,7 +457,7 @@ taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t *a, taco_
 int64_t taco_gated_linear_workspace(int64_t rows, int64_t inner, int64_t hidden)
 {
     int64_t ny = 0, nx = 0, nw = 0;
-    if (check_gated(rows, inner, hidden, &ny, &nx, &nw) != TACO_OK)
+    if (check_gated(rows, inner, hidden, &ny, &nx, &nw) != TACO_OK || !gated_sum_in_range(hidden))
         return -1;
     return gated_workspace(rows, inner, hidden);
 }
@@ -470,7 +470,7 @@ taco_status_t taco_gated_linear(const taco_gated_linear_args_t *a, taco_stream_t
     taco_status_t st = check_gated(a->rows, a->inner, a->hidden, &ny, &nx, &nw);
     if (st == TACO_OK && a->packed)
         st = check_gated_records(a->inner, a->block, a->code);
-    if (st == TACO_OK && a->hidden == 0)
+    if (st == TACO_OK && (a->hidden == 0 || !gated_sum_in_range(a->hidden)))
         st = TACO_ERR_BAD_SHAPE;
     if (st != TACO_OK || ny == 0)
         return st;
@@ -499,7 +499,7 @@ taco_status_t taco_gated_linear(const taco_gated_linear_args_t *a, taco_stream_t
 int64_t taco_gated_linear_backward_workspace(int64_t rows, int64_t inner, int64_t hidden)
 {
     int64_t ny = 0, nx = 0, nw = 0;
-    if (check_gated(rows, inner, hidden, &ny, &nx, &nw) != TACO_OK)
+    if (check_gated(rows, inner, hidden, &ny, &nx, &nw) != TACO_OK || (hidden > 0 && !gated_sum_in_range(2 * inner)))
         return -1;
     return (hidden > 0 && rows > 0 ? gated_input_grad_workspace(rows, inner, hidden) : 0) + 8 * column_parts(rows) * inner;
 }
@@ -517,6 +517,8 @@ taco_status_t taco_gated_linear_backward(const taco_gated_linear_backward_args_t
     if (st != TACO_OK)
         return st;
     const bool input = a->weight || a->dx;
+    if (input && !gated_sum_in_range(2 * a->inner))
+        return TACO_ERR_BAD_SHAPE;
     const int64_t product = input && a->rows > 0 ? gated_input_grad_workspace(a->rows, a->inner, a->hidden) : 0;
     const int64_t sums = a->dbias ? 8 * column_parts(a->rows) * a->inner : 0, need = product + sums;
     if (a->rows != 0) {

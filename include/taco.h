@@ -391,7 +391,7 @@ TACO_API taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t 
  * then, blocks 32, 64 and 128).  The activation: silu(g) = g / (1 + exp(-g)),
  * +infinity for g = +infinity and NaN for -infinity as GELU's is, or GELU in either
  * form.  bf16 and f16; x and W have one type.
- * 1 <= hidden < 2^31 - 256, rows < 2^31 - 256, inner < 2^30 - 256
+ * 1 <= hidden <= 2^24, rows < 2^31 - 256, inner < 2^30 - 256
  * (TACO_ERR_BAD_SHAPE).  rows == 0 or inner == 0 launches nothing.  Rows of x and W
  * whose hidden is no multiple of 8 are first copied to the workspace.
  */
@@ -423,8 +423,9 @@ TACO_API taco_status_t taco_gated_linear(const taco_gated_linear_args_t *args, t
  *   dz_gate = dy z_up act'(z_gate), dz_up = dy act(z_gate), dx = dz W,
  *   dbias = sum over rows of dz (before rounding), and y again.
  * dx is the product of dz as it is written (rounded to dtype).  The weight's
- * gradient dz^T X is taco_weight_grad's (`out` = 2 inner).  inner >= 1, and
- * hidden >= 1 where dx is wanted; the ranges are those above.
+ * gradient dz^T X is taco_weight_grad's (`out` = 2 inner).  inner >= 1, and where
+ * dx is wanted inner <= 2^23 and 1 <= hidden < 2^31 - 256; the ranges are those
+ * above otherwise.
  */
 typedef struct taco_gated_linear_backward_args {
     const void *dy;             /* in:  [rows, inner] */
