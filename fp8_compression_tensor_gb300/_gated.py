@@ -5,7 +5,7 @@ training operators of _training.py (include/taco.h):
     g = rmsnorm_backward(dy, r.rstd, weight, packed=r.packed)        # g.dx, g.dweight
     r = gated_linear(x, weight, checkpoint=True)                     # r.y, r.packed
     g = gated_linear_backward(dy, r.packed, weight)                  # g.dz, g.dx, g.dbias, g.y
-    dw = weight_grad(g.dz, packed, hidden)                           # the projections' weights, X kept as records
+    dw = weight_grad(g.dz, packed, hidden)                           # the projections' weights, X kept as records (bf16)
 
 Argument marshalling only.  No call records an autograd graph: the forward and
 backward calls are for a torch.autograd.Function, as in
@@ -254,7 +254,8 @@ def gated_linear_backward(dy: torch.Tensor, packed: torch.Tensor, weight: Option
     input's gradient dx = dz weight; with bias_dtype the sum of dz over rows in
     that type; with recompute the output y again, for the next layer's weight
     gradient.  The weight's own gradient is weight_grad(dz, records of x,
-    hidden)."""
+    hidden), which takes bf16 alone: for f16 it is a product of dz with x as it
+    was, outside this package."""
     act = _activation(activation)
     if bias_dtype is not None and bias_dtype not in DTYPES:
         raise TypeError(f"bias_dtype must be bfloat16, float16 or float32, got {bias_dtype}")

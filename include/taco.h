@@ -423,7 +423,8 @@ TACO_API taco_status_t taco_gated_linear(const taco_gated_linear_args_t *args, t
  *   dz_gate = dy z_up act'(z_gate), dz_up = dy act(z_gate), dx = dz W,
  *   dbias = sum over rows of dz (before rounding), and y again.
  * dx is the product of dz as it is written (rounded to dtype).  The weight's
- * gradient dz^T X is taco_weight_grad's (`out` = 2 inner).  inner >= 1, and where
+ * gradient dz^T X is taco_weight_grad's (`out` = 2 inner), which takes bf16 alone:
+ * f16 has dz, dx, dbias and y here, and no weight gradient from records.  inner >= 1, and where
  * dx is wanted inner <= 2^23 and 1 <= hidden < 2^31 - 256; the ranges are those
  * above otherwise.
  */
