@@ -20,9 +20,19 @@
 // warp 2 owns tensor memory, warps 4-15 are the epilogue: warp w reads lanes 32 (w
 // % 4) .., a row a thread.  Without records the first eight of them take 64 columns
 // of y (128 of dx) each; with records the first four take y, the others the gate's
-// and the up projection's records: 333 x 1000 x 2048 f16 with biases takes 12.9 us
-// and 8192 x 1024 x 4096 with biases 97, with eight warps that do both in turn 13.9
-// and 116.
+// and the up projection's records.  That took 8192 x 1024 x 4096 with biases from 116
+// to 97 us and 333 x 1000 x 2048 f16 with biases from 13.9 to 12.9, against eight
+// warps that do both in turn; with what followed they take 92 and (tiles of 64
+// columns) 10.1.
+//
+// One accumulator holds a tile's whole sum.  The tensor core cuts each addition, so
+// a sum comes out short by 1.0e-9 of its size a term: measured 8.2e-6 over 8192
+// terms, 3.3e-5 over 32768, 1.0e-3 over 2^20, and an eighth of it where a cluster
+// cuts the sum (taco_gated_serve.cu).  Outputs have 16 bits, whose rounding alone takes
+// 2.1e-4 (f16) or 1.7e-3 (bf16) of one.  The weight gradient, which writes binary32
+// and sums over tokens, ends an accumulator after 1024 of them and adds up in
+// registers; here that would cost reads and registers for what the outputs' rounding
+// hides at the widths of models.
 #include <algorithm>
 #include <climits>
 
@@ -162,7 +172,7 @@ __device__ __forceinline__ void write_staged(uint32_t buffer, const void *map, c
 // The bias of a tile's 128 columns from c on, of projection k (0 gate, 1 up), as
 // binary32 at `to` in shared memory (zeros outside).  It is fetched ahead of the
 // accumulator's wait: loaded a column a lane where it is added, 333 x 1000 x 2048 with
-// records took 17 us.
+// records (tiles of 128 columns) took 17 us against 13.
 __device__ __forceinline__ void stage_bias(uint32_t to, const TileArgs &a, int k, int64_t c)
 {
     const int lane = threadIdx.x & 31;
@@ -667,11 +677,12 @@ cudaError_t launch_gated(const GatedArgs &a, uint32_t *fault, int sms, cudaStrea
 // 76 pairs take the tiles in waves; those of the last wave may be cut so that its
 // pairs finish together.  In units of 64 along K (0.27 us a tile) a cut costs what
 // its sums take to be written and read again (512 KB a range, 0.2) and the kernel
-// that joins them (11): taken where that leaves less than 85%.  257 x 1024 x 2752
-// (8 tiles) takes 16.0 us in nine ranges and 30.3 whole, 1000 x 2048 x 8192 (32
-// tiles) 77 in two and 99 whole; 8192 x 4096 x 16384 (56 tiles in the last wave of
-// 7) and 640 x 5120 x 13824 (60 tiles) would take 1411 and 154 cut, 1416 and 146
-// whole.
+// that joins them (11): taken where that leaves less than 85%.  With
+// the kernel that makes dz, 257 x 1024 x 2752 (8 tiles) takes 15.0 us in the eight
+// ranges that this picks (15.2 in seven, 14.6 in nine) and 29.0 whole, 1000 x 2048 x
+// 8192 (32 tiles) 65.6 in two and 88.8 whole; 640 x 5120 x 13824 (60 tiles) would
+// take 153 cut and takes 143 whole, 8192 x 4096 x 16384 (56 tiles in the last wave
+// of 7) 1342 to 1419 either way.
 struct Split {
     int64_t tiles, tail, splits;
 };

@@ -393,7 +393,9 @@ TACO_API taco_status_t taco_rmsnorm_backward(const taco_rmsnorm_backward_args_t 
  * form.  bf16 and f16; x and W have one type.
  * 1 <= hidden <= 2^24, rows < 2^31 - 256, inner < 2^30 - 256
  * (TACO_ERR_BAD_SHAPE).  rows == 0 or inner == 0 launches nothing.  Rows of x and W
- * whose hidden is no multiple of 8 are first copied to the workspace.
+ * whose hidden is no multiple of 8 are first copied to the workspace.  The products'
+ * binary32 sums are the tensor core's, which cuts each addition: they come out short
+ * by up to 1.1e-9 of their size a term, 3.5e-5 over 32768 terms.
  */
 typedef enum taco_activation {
     TACO_ACTIVATION_SILU = 0,
