@@ -116,7 +116,8 @@ __device__ __forceinline__ void gelu_both2(float2 u, float2 &y, float2 &slope)
 
 // silu(g) = g p with p = 1 / (1 + exp(-g)), and its slope p (1 + g (1 - p)).  The
 // exponential's error grows with the rounding of g log2(e), to 1e-6 of p at g =
-// -16; above, 1 / (1 + e) damps it.  g bounded by 80 in the slope keeps +infinity
+// -16; above, 1 / (1 + e) damps it.  Below g = -87.3 p is flushed to zero, and g p,
+// smaller than 2^-119 there, with it.  g bounded by 80 in the slope keeps +infinity
 // from meeting 1 - p = 0 (slope 1); -infinity meets p = 0 in both (NaN).
 __device__ __forceinline__ float2 silu_gate2(float2 g)
 {
